@@ -20,7 +20,7 @@
  *   - All tensor pointers are DEVICE pointers on the current CUDA device, row-major and
  *     contiguous, 16-byte aligned.  BF16 tensors are raw bfloat16 bit patterns.
  *   - The caller owns every buffer.  The library never allocates, frees or synchronises
- *     (moe_get_error is the one call that synchronises its stream).
+ *     (the *_get_error calls synchronise their stream).
  *   - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default stream).
  *   - Arguments are validated on the host before anything is enqueued; on error nothing
  *     is launched and the status says why.  T == 0 (moe_fused_forward) and M == 0
@@ -49,7 +49,9 @@ typedef enum {
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1 } moe_act_t;
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP32 = 1 } moe_dtype_t;
+/* The 8-bit types (E4M3: largest value 448, E5M2: 57344) are those of the expert operators'
+ * quantised operands only. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP32 = 1, MOE_DT_E4M3 = 2, MOE_DT_E5M2 = 3 } moe_dtype_t;
 /* Execution path of moe_fused_forward.  AUTO picks by token count (see
  * moe_select_path).  SMALL streams only the routed experts' weights with CUDA-core dot
  * products spread over all SMs; LARGE runs the grouped tcgen05 tensor-core GEMMs. */
@@ -302,6 +304,120 @@ moe_status_t moe_noalloc_get_error(int* code, void* stream);
  * Returns MOE_ERR_DEVICE when code != 0, MOE_OK otherwise, MOE_ERR_CUDA if the copy fails.
  * ---------------------------------------------------------------------------------- */
 moe_status_t moe_get_error(void* ws, int* code, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Expert operators: the steps between moe_permute and the layer's output one by one, with
+ * their gradients and with 8-bit operands, for training an expert layer and for serving
+ * 8-bit weights.  A run of them is
+ *   moe_router_topk -> moe_permute -> moe_dispatch_quantize -> moe_product_activation
+ *   -> moe_product -> moe_combine.
+ * They take no workspace.  Calls on different streams are safe when their outputs are
+ * distinct.  Outputs must not overlap inputs.  Zero rows are valid and launch nothing
+ * (except where an output of zeros is due: moe_combine without kept slots, and
+ * moe_product_weight_grad without rows).  `dtype` is MOE_DT_BF16 or MOE_DT_FP32, `fp8`
+ * MOE_DT_E4M3 or MOE_DT_E5M2.
+ *
+ * Rows sorted by expert: P rows, expert e's at [offsets[e], offsets[e + 1]).
+ * `offsets` [E + 1] int32 as moe_permute writes them, or NULL for one expert (E == 1) with
+ * all P rows.  Values are clamped to [0, P]; rows from offsets[E] on are not read, and
+ * are left as they were in the outputs.  Limits: P <= MOE_MAX_ROWS, E <= MOE_MAX_EXPERTS,
+ * every feature count <= MOE_MAX_FEATURES.
+ * ---------------------------------------------------------------------------------- */
+#define MOE_MAX_ROWS (MOE_MAX_TOKENS * 8)
+#define MOE_MAX_FEATURES (1 << 20)
+#define MOE_QUANT_BLOCK 128
+
+/* moe_dispatch -- tokens to their experts' rows: xs[inv[k * M + m], :] = x[m, :].
+ *   x [M, H], xs [P, H] of `dtype`; H a multiple of 8.
+ *   inv [K * M] int32, as moe_permute writes it.  A value outside [0, P) is a dropped slot
+ *   and is skipped; the others must be distinct.  Rows that no slot names are left as they
+ *   were.  Its gradient is moe_combine with weights == NULL. */
+moe_status_t moe_dispatch(const void* x, int dtype, int M, int K, int H, const int32_t* inv, int P, void* xs,
+                          void* stream);
+
+/* moe_combine -- the experts' rows back to their tokens:
+ *   y[m, :] = sum over k of weights[m, k] * ys[inv[k * M + m], :], in FP32 in ascending k,
+ *   rounded once.  weights [M, K] FP32, or NULL for ones (the gradient of moe_dispatch).
+ *   Dropped slots (as in moe_dispatch) add nothing, whatever their weight.  Non-dropped
+ *   entries of inv may repeat.  Every row of y is written. */
+moe_status_t moe_combine(const void* ys, int dtype, int M, int K, int H, const int32_t* inv, int P,
+                         const float* weights, void* y, void* stream);
+
+/* moe_combine_backward -- from dy [M, H]: dys[inv[k * M + m], :] = weights[m, k] * dy[m, :]
+ * (rows that no slot names are left as they were), and
+ * dweights[m, k] = the FP32 dot product of dy[m, :] and ys[inv[k * M + m], :], 0 for a
+ * dropped slot.  inv as in moe_dispatch. */
+moe_status_t moe_combine_backward(const void* dy, const void* ys, int dtype, int M, int K, int H, const int32_t* inv,
+                                  int P, const float* weights, void* dys, float* dweights, void* stream);
+
+/* 8-bit blocks.  A block whose largest magnitude is a (taken as at least 2^-96) has the
+ * FP32 scale s = a / fmax and the values q = round(v * f), f = fmax / a, every operation
+ * in FP32 rounded to nearest even (q to the 8-bit type); v is about s * q.  A block with an
+ * infinity or a NaN gets a scale that is one, and its values of it become NaN.
+ * Feature counts are multiples of 16.  */
+/* Rows: one scale per row and MOE_QUANT_BLOCK columns (the last block may be shorter).
+ *   x [R, C] of `dtype`; q [R, C] of `fp8`; scales [R, ceil(C / 128)] FP32. */
+moe_status_t moe_quantize_rows(const void* x, int dtype, int R, int C, int fp8, void* q, float* scales,
+                               void* stream);
+/* moe_dispatch and moe_quantize_rows in one pass: each token is read and rounded once.
+ *   q [P, H], scales [P, ceil(H / 128)]; H a multiple of 16. */
+moe_status_t moe_dispatch_quantize(const void* x, int dtype, int M, int K, int H, const int32_t* inv, int P, int fp8,
+                                   void* q, float* scales, void* stream);
+/* Blocks of MOE_QUANT_BLOCK x MOE_QUANT_BLOCK of E matrices (weights).
+ *   w [E, N, C]; q [E, N, C]; scales [E, ceil(N / 128), ceil(C / 128)]. */
+moe_status_t moe_quantize_blocks(const void* w, int dtype, int E, int N, int C, int fp8, void* q, float* scales,
+                                 void* stream);
+/* Columns: one scale per column and MOE_QUANT_BLOCK rows of an expert, for
+ * moe_product_weight_grad.  Each expert's rows start a new block; its last block is filled
+ * up with zero rows.  x [P, C]; with B = moe_column_blocks(P, E): q [B * 128, C] and
+ * scales [B, C], of which the sum over experts of ceil(rows / 128) blocks is written and the
+ * rest left as it was. */
+int moe_column_blocks(int P, int E);
+moe_status_t moe_quantize_columns(const void* x, int dtype, int P, int C, const int32_t* offsets, int E, int fp8,
+                                  void* q, float* scales, void* stream);
+
+/* moe_activation -- between an expert's two products.  act: moe_act_t.
+ *   MOE_ACT_SWIGLU: y [P, 2I] = gate, up;  h = silu(gate) * up.   MOE_ACT_RELU2: y [P, I].
+ *   h [P, I] of `dtype`; I a multiple of 8.
+ * _quantize: h goes through moe_quantize_rows instead, from its FP32 value: q [P, I] of `fp8`,
+ * scales [P, ceil(I / 128)]; I a multiple of 16.
+ * _backward: dy (the shape of y) from y and dh [P, I]. */
+moe_status_t moe_activation(const void* y, int dtype, int act, int P, int I, void* h, void* stream);
+moe_status_t moe_activation_quantize(const void* y, int dtype, int act, int P, int I, int fp8, void* q, float* scales,
+                                     void* stream);
+moe_status_t moe_activation_backward(const void* y, const void* dh, int dtype, int act, int P, int I, void* dy,
+                                     void* stream);
+
+/* moe_product -- each row times its expert's 8-bit weights, y[p, n] = sum_c x[p, c] w[e, n, c]:
+ *   xq [P, C] of x_fp8 and x_scales as moe_quantize_rows writes them; wq [E, N, C] MOE_DT_E4M3 and
+ *   w_scales as moe_quantize_blocks does; y [P, N] of out_dtype.  C and N multiples of 16.
+ *   The products of a block are summed on the tensor cores, the blocks in FP32, and the
+ *   result is rounded once. */
+moe_status_t moe_product(const void* xq, const float* x_scales, int x_fp8, const void* wq, const float* w_scales,
+                         int P, int N, int C, const int32_t* offsets, int E, int out_dtype, void* y, void* stream);
+/* moe_product, the activation of its FP32 sums, and moe_quantize_rows of that, without
+ * storing the product: wq [E, 2I, C] (MOE_ACT_SWIGLU: rows [0, I) gate, [I, 2I) up) or
+ * [E, I, C] (MOE_ACT_RELU2); hq [P, I] of h_fp8, h_scales [P, ceil(I / 128)]. */
+moe_status_t moe_product_activation(const void* xq, const float* x_scales, int x_fp8, const void* wq,
+                                    const float* w_scales, int P, int I, int C, const int32_t* offsets, int E,
+                                    int act, int h_fp8, void* hq, float* h_scales, void* stream);
+/* Gradient of moe_product's input, dx[p, c] = sum_n dy[p, n] w[e, n, c], from the same
+ * weights as they lie: dyq [P, N] of dy_fp8 and dy_scales as moe_quantize_rows writes them;
+ * dx [P, C] of out_dtype. */
+moe_status_t moe_product_input_grad(const void* dyq, const float* dy_scales, int dy_fp8, const void* wq,
+                                    const float* w_scales, int P, int N, int C, const int32_t* offsets, int E,
+                                    int out_dtype, void* dx, void* stream);
+/* Gradient of moe_product's weights, dw[e, n, c] = sum over the rows p of e of dy[p, n] x[p, c]:
+ * dyq [B * 128, N], xq [B * 128, C] and their scales [B, N], [B, C] as moe_quantize_columns
+ * writes them with the same offsets (without offsets, all B blocks are the one expert's).  dw [E, N, C] of out_dtype; accumulate 1: added to dw (in FP32, rounded
+ * once), 0: written, zeros for an expert without rows. */
+moe_status_t moe_product_weight_grad(const void* dyq, const float* dy_scales, int dy_fp8, const void* xq,
+                                     const float* x_scales, int x_fp8, int B, int N, int C, const int32_t* offsets,
+                                     int E, int out_dtype, int accumulate, void* dw, void* stream);
+/* Read and clear the products' device error word of the current device (MOE_DEVERR_WAIT_TIMEOUT:
+ * a bounded wait gave up and outputs are incomplete).  Synchronises `stream`.  Returns as
+ * moe_get_error. */
+moe_status_t moe_product_get_error(int* code, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* moe_status_string(moe_status_t s);

@@ -20,7 +20,7 @@ SCORE = {"softmax": 0, "sigmoid": 1}
 ACT = {"swiglu": 0, "relu2": 1}
 PATH = {"auto": 0, "small": 1, "large": 2}
 SCHEDULE = {"auto": 0, "static": 1, "dynamic": 2}  # moe_sched_t
-DT_BF16, DT_FP32 = 0, 1
+DT_BF16, DT_FP32, DT_E4M3, DT_E5M2 = range(4)  # moe_dtype_t
 DEVERR_BAD_EXPERT_ID, DEVERR_WAIT_TIMEOUT, DEVERR_BAD_INDEX, DEVERR_ROUTER_BOUND = 0x1, 0x2, 0x4, 0x8
 WS_TOPK_IDS, WS_TOPK_W, WS_OFFSETS, WS_PERM = range(4)
 
@@ -29,7 +29,12 @@ EXPORTS = ("moe_router_topk", "moe_permute_workspace_size", "moe_permute", "moe_
            "moe_select_path", "moe_fused_forward", "moe_fused_forward_launches", "moe_fused_forward_plan",
            "moe_token_tiles", "moe_trace_size",
            "moe_workspace_region", "moe_fused_forward_timed", "moe_fused_forward_noalloc",
-           "moe_noalloc_get_error", "moe_get_error", "moe_status_string")
+           "moe_noalloc_get_error", "moe_get_error", "moe_status_string",
+           # expert operators (bound in experts.py)
+           "moe_dispatch", "moe_combine", "moe_combine_backward", "moe_quantize_rows", "moe_dispatch_quantize",
+           "moe_quantize_blocks", "moe_column_blocks", "moe_quantize_columns", "moe_activation",
+           "moe_activation_quantize", "moe_activation_backward", "moe_product", "moe_product_activation",
+           "moe_product_input_grad", "moe_product_weight_grad", "moe_product_get_error")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m mixture_experts_layer_35_b200.build`")
