@@ -17,8 +17,8 @@
 // (contraction over C), the input gradient MN-major (contraction over N), and the weight
 // gradient reads both operands MN-major, so nothing is transposed.
 //
-// Warps: 0 TMA producer, 1 TMEM allocator and MMA issuer, 2-9 epilogue (warp w reads TMEM
-// lanes of quarter w % 4 and one half of the columns).  One persistent CTA per SM; tiles go
+// Warps: 0 TMA producer, 1 TMEM allocator and MMA issuer, 4-11 epilogue (warp w reads TMEM
+// lanes of quarter w % 4 and one half of the columns); 2 and 3 only fill the warpgroup.  One persistent CTA per SM; tiles go
 // round-robin, inside an expert in bands of 16 row tiles, column tiles outer, so that the
 // CTAs at work share weights and rows in L2.
 #include "experts.cuh"
@@ -31,7 +31,11 @@ __device__ int g_product_error;  // MOE_DEVERR_* bits of the products on this de
 constexpr int BM = 128, BKB = 128;  // tile rows; bytes (= values) of one block along the contraction
 constexpr int kBand = 16;           // row tiles that share a pass over the weights
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+// With 128 sums a thread (BN = 256) the epilogue warpgroups take registers from the first
+// one: 128 * 40 + 256 * 224 of the 384 * 168 that a block is launched with.
+constexpr int kRegsIssue = 40, kRegsEpilogue = 224;
+constexpr int kRegsLaunch = (128 * kRegsIssue + 256 * kRegsEpilogue + kThreads - 1) / kThreads;
 constexpr int A_BYTES = BM * BKB;
 constexpr int kStageOut = 2048;  // staging of one epilogue warp: 32 rows x 64 bytes
 
@@ -45,6 +49,7 @@ struct Cfg {
     static constexpr int kFit = (int)((227 * 1024 - 1024 - kMeta - kEpiWarps * kStageOut) / kStageBytes);
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kStageOut + kMeta;
+    static constexpr bool kMoveRegs = BN == 256;
     static constexpr int kCpt = BN / 2;  // columns of a tile per epilogue thread
     static_assert(kStages >= 3, "ring too shallow");
     static_assert(8 * (2 * kStages + 2 * kBufs + 4) + 8 <= 512, "barrier block");
@@ -77,6 +82,49 @@ __device__ __forceinline__ void tc_mma_fp8(uint32_t tmem_d, uint64_t adesc, uint
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_set_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_set_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Waits for this thread's TMEM loads; the values loaded cannot be used before it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31]));
+}
+// Two FP32 operations in one instruction, on register pairs.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
+    lo = __uint_as_float(a);
+    hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 struct Tile {
@@ -187,79 +235,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nct = cdiv(a.cols, kColStep);
     const int total = KIND == PK_WEIGHT_GRAD ? a.E * cdiv(a.rows, BM) * nct : s_first[a.E] * nct;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-                const Tile t = decode<KIND>(a, s_off, s_first, nct, tile);
-                const int c0 = t.ct * kColStep;
-                const int abox = KIND == PK_WEIGHT_GRAD ? 1 : cdiv(t.n, a_rows);
-                const uint32_t bytes = (KIND == PK_WEIGHT_GRAD ? A_BYTES : abox * a_rows * BKB) + C::kBBytes;
-                for (int kb = 0; kb < t.nk; ++kb, ++it) {
-                    const int s = it % C::kStages;
-                    if (!mbar_wait(empty_bar(s), ((uint32_t)(it / C::kStages) & 1u) ^ 1u, abort_flag, err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = base_u32 + (uint32_t)s * C::kStageBytes, sb = sa + A_BYTES;
-                    const uint32_t bar = full_bar(s);
-                    mbar_expect_tx(bar, bytes);
-                    if (KIND == PK_WEIGHT_GRAD) {
-                        const int r = (t.blk0 + kb) * BKB;
-                        tma_load_2d(sa, &tm_a, bar, t.row0, r);
-                        for (int j = 0; j < BN / 128; ++j) tma_load_2d(sb + j * 16384, &tm_b, bar, c0 + j * 128, r);
-                    } else {
-                        for (int j = 0; j < abox; ++j)
-                            tma_load_2d(sa + j * a_rows * BKB, &tm_a, bar, kb * BKB, t.row0 + j * a_rows);
-                        if (KIND == PK_INPUT_GRAD) {
-                            for (int j = 0; j < BN / 128; ++j)
-                                tma_load_3d(sb + j * 16384, &tm_b, bar, c0 + j * 128, kb * BKB, t.e);
-                        } else if (kSwiglu) {
-                            tma_load_3d(sb, &tm_b, bar, kb * BKB, c0, t.e);
-                            tma_load_3d(sb + (BN / 2) * BKB, &tm_b, bar, kb * BKB, a.up + c0, t.e);
+    if (warp < 4) {
+        if (C::kMoveRegs) regs_set_down<kRegsIssue>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ TMA producer
+            if (lane == 0) {
+                int it = 0;
+                bool ok = true;
+                for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+                    const Tile t = decode<KIND>(a, s_off, s_first, nct, tile);
+                    const int c0 = t.ct * kColStep;
+                    const int abox = KIND == PK_WEIGHT_GRAD ? 1 : cdiv(t.n, a_rows);
+                    const uint32_t bytes = (KIND == PK_WEIGHT_GRAD ? A_BYTES : abox * a_rows * BKB) + C::kBBytes;
+                    for (int kb = 0; kb < t.nk; ++kb, ++it) {
+                        const int s = it % C::kStages;
+                        if (!mbar_wait(empty_bar(s), ((uint32_t)(it / C::kStages) & 1u) ^ 1u, abort_flag, err)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sa = base_u32 + (uint32_t)s * C::kStageBytes, sb = sa + A_BYTES;
+                        const uint32_t bar = full_bar(s);
+                        mbar_expect_tx(bar, bytes);
+                        if (KIND == PK_WEIGHT_GRAD) {
+                            const int r = (t.blk0 + kb) * BKB;
+                            tma_load_2d(sa, &tm_a, bar, t.row0, r);
+                            for (int j = 0; j < BN / 128; ++j) tma_load_2d(sb + j * 16384, &tm_b, bar, c0 + j * 128, r);
                         } else {
-                            tma_load_3d(sb, &tm_b, bar, kb * BKB, c0, t.e);
+                            for (int j = 0; j < abox; ++j)
+                                tma_load_2d(sa + j * a_rows * BKB, &tm_a, bar, kb * BKB, t.row0 + j * a_rows);
+                            if (KIND == PK_INPUT_GRAD) {
+                                for (int j = 0; j < BN / 128; ++j)
+                                    tma_load_3d(sb + j * 16384, &tm_b, bar, c0 + j * 128, kb * BKB, t.e);
+                            } else if (kSwiglu) {
+                                tma_load_3d(sb, &tm_b, bar, kb * BKB, c0, t.e);
+                                tma_load_3d(sb + (BN / 2) * BKB, &tm_b, bar, kb * BKB, a.up + c0, t.e);
+                            } else {
+                                tma_load_3d(sb, &tm_b, bar, kb * BKB, c0, t.e);
+                            }
                         }
                     }
                 }
             }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = idesc_fp8(a.a_e5m2, a.b_e5m2, kAmn, kBmn, BN);
-            int it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-                const Tile t = decode<KIND>(a, s_off, s_first, nct, tile);
-                for (int kb = 0; kb < t.nk; ++kb, ++it) {
-                    const int s = it % C::kStages, b = it % C::kBufs;
-                    if (!mbar_wait(tempty_bar(b), ((uint32_t)(it / C::kBufs) & 1u) ^ 1u, abort_flag, err) ||
-                        !mbar_wait(full_bar(s), (uint32_t)(it / C::kStages) & 1u, abort_flag, err)) {
-                        ok = false;
-                        break;
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                const uint32_t idesc = idesc_fp8(a.a_e5m2, a.b_e5m2, kAmn, kBmn, BN);
+                int it = 0;
+                bool ok = true;
+                for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+                    const Tile t = decode<KIND>(a, s_off, s_first, nct, tile);
+                    for (int kb = 0; kb < t.nk; ++kb, ++it) {
+                        const int s = it % C::kStages, b = it % C::kBufs;
+                        if (!mbar_wait(tempty_bar(b), ((uint32_t)(it / C::kBufs) & 1u) ^ 1u, abort_flag, err) ||
+                            !mbar_wait(full_bar(s), (uint32_t)(it / C::kStages) & 1u, abort_flag, err)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = base_u32 + (uint32_t)s * C::kStageBytes, sb = sa + A_BYTES;
+                        const uint32_t d = tmem_base + (uint32_t)(b * BN);
+    #pragma unroll
+                        for (int kk = 0; kk < BKB / 32; ++kk) {
+                            const uint64_t ad = kAmn ? sdesc_sw128_mn(sa + kk * 4096) : sdesc_sw128(sa + kk * 32);
+                            const uint64_t bd = kBmn ? sdesc_sw128_mn(sb + kk * 4096) : sdesc_sw128(sb + kk * 32);
+                            tc_mma_fp8(d, ad, bd, idesc, kk > 0);
+                        }
+                        tc_commit(empty_bar(s));
+                        tc_commit(tfull_bar(b));
                     }
-                    tc_fence_after();
-                    const uint32_t sa = base_u32 + (uint32_t)s * C::kStageBytes, sb = sa + A_BYTES;
-                    const uint32_t d = tmem_base + (uint32_t)(b * BN);
-#pragma unroll
-                    for (int kk = 0; kk < BKB / 32; ++kk) {
-                        const uint64_t ad = kAmn ? sdesc_sw128_mn(sa + kk * 4096) : sdesc_sw128(sa + kk * 32);
-                        const uint64_t bd = kBmn ? sdesc_sw128_mn(sb + kk * 4096) : sdesc_sw128(sb + kk * 32);
-                        tc_mma_fp8(d, ad, bd, idesc, kk > 0);
-                    }
-                    tc_commit(empty_bar(s));
-                    tc_commit(tfull_bar(b));
                 }
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        if (C::kMoveRegs) regs_set_up<kRegsEpilogue>();
+        const int q = warp & 3, half = (warp - 4) >> 2;
         const int r = q * 32 + lane;  // this thread's row of the tile
-        uint8_t* stage = staging + (warp - 2) * kStageOut;
+        uint8_t* stage = staging + (warp - 4) * kStageOut;
         const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
         int it = 0, ntile = 0;
         bool ok = true;
@@ -268,17 +320,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = t.ct * kColStep;
             const bool live = q * 32 < t.n;  // any row of this warp in the tile
             const bool mine = r < t.n;
-            float acc[C::kCpt];
+            uint64_t acc2[C::kCpt / 2];  // the sums, in pairs of neighbouring columns
 #pragma unroll
-            for (int j = 0; j < C::kCpt; ++j) acc[j] = 0.0f;
-            // Scales: sa of this thread's row; sb of the weight blocks of its columns.
+            for (int j = 0; j < C::kCpt / 2; ++j) acc2[j] = 0;
+            // Scales of a block, loaded one block ahead: ra of this thread's row; rb of the weight
+            // block of its columns.  SwiGLU's up features start anywhere in a weight block: the
+            // first up_cut of them lie in block up0 (ru), the others in the next (rv).  Weight
+            // gradient: each lane loads four of the warp's column scales (rc), and passes them
+            // through shared memory.
             const float* sa = nullptr;
             const float* sb = nullptr;
-            int sa_step = 1, sb_step = 1, up0 = 0, up_cut = 0;
+            const float* su = nullptr;
+            const float* sv = nullptr;
+            int sa_step = 1, sb_step = 1, up_cut = 0;
+            const bool cols_in = c0 + half * C::kCpt + 4 * lane < a.cols && 4 * lane < C::kCpt;
             if (KIND == PK_WEIGHT_GRAD) {
                 sa = a.sa + (size_t)t.blk0 * a.rows + t.row0 + (mine ? r : 0);
                 sa_step = a.rows;
-                sb = a.sb + (size_t)t.blk0 * a.cols;
+                sb = a.sb + (size_t)t.blk0 * a.cols + (cols_in ? c0 + half * C::kCpt + 4 * lane : 0);
                 sb_step = a.cols;
             } else {
                 sa = a.sa + (size_t)(t.row0 + (mine ? r : 0)) * a.nbl;
@@ -288,63 +347,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     const int nb = min((c0 + (kSwiglu ? half * (C::kCpt / 2) : half * C::kCpt)) / 128, a.wn - 1);
                     sb = a.sb + ((size_t)t.e * a.wn + nb) * a.wk;
-                    if (kSwiglu) {  // up features start anywhere in a block: the first up_cut of them are in block up0
+                    if (kSwiglu) {
                         const int u = a.up + c0 + half * (C::kCpt / 2);
-                        up0 = min(u / 128, a.wn - 1);
+                        const int up0 = min(u / 128, a.wn - 1);
                         up_cut = (u / 128 + 1) * 128 - u;
+                        su = a.sb + ((size_t)t.e * a.wn + up0) * a.wk;
+                        sv = a.sb + ((size_t)t.e * a.wn + min(up0 + 1, a.wn - 1)) * a.wk;
                     }
                 }
             }
+            float ra = 0.0f, rb = 0.0f, ru = 0.0f, rv = 0.0f;
+            float4 rc = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto load_scales = [&](int kb) {
+                if (!live) return;
+                ra = __ldg(sa + (size_t)kb * sa_step);
+                if (KIND == PK_WEIGHT_GRAD) {
+                    if (cols_in) rc = __ldg(reinterpret_cast<const float4*>(sb + (size_t)kb * sb_step));
+                } else {
+                    rb = __ldg(sb + (size_t)kb * sb_step);
+                    if (kSwiglu) {
+                        ru = __ldg(su + kb);
+                        rv = __ldg(sv + kb);
+                    }
+                }
+            };
+            if (t.nk > 0) load_scales(0);
             for (int kb = 0; kb < t.nk; ++kb, ++it) {
                 const int b = it % C::kBufs;
-                const float s0 = live ? __ldg(sa + (size_t)kb * sa_step) : 0.0f;
-                float s1 = 0.0f, u1 = 0.0f, u2 = 0.0f;
-                if (KIND != PK_WEIGHT_GRAD) s1 = s0 * __ldg(sb + (size_t)kb * sb_step);
-                if (kSwiglu) {
-                    const float* up = a.sb + ((size_t)t.e * a.wn + up0) * a.wk + kb;
-                    u1 = s0 * __ldg(up);
-                    u2 = up0 + 1 < a.wn ? s0 * __ldg(up + a.wk) : 0.0f;
+                const float s0 = ra;
+                const uint64_t s1 = KIND == PK_WEIGHT_GRAD ? pair(s0, s0) : pair(s0 * rb, s0 * rb);
+                const uint64_t u1 = pair(s0 * ru, s0 * ru), u2 = pair(s0 * rv, s0 * rv);
+                if (KIND == PK_WEIGHT_GRAD) {
+                    __syncwarp();  // the last block's scales have been read
+                    if (4 * lane < C::kCpt) reinterpret_cast<float4*>(stage)[lane] = rc;
+                    __syncwarp();
                 }
+                if (kb + 1 < t.nk) load_scales(kb + 1);
                 if (!mbar_wait(tfull_bar(b), (uint32_t)(it / C::kBufs) & 1u, abort_flag, err)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (live) {
+                    // 32 columns at a time, the next ones loading while these are added
+                    uint32_t v[2][32];
+                    auto column = [&](int j0) {  // first TMEM column of piece j0 of this thread
+                        if (!kSwiglu) return half * C::kCpt + j0;
+                        return (j0 >= C::kCpt / 2 ? BN / 2 - C::kCpt / 2 : 0) + half * (C::kCpt / 2) + j0;
+                    };
+                    const uint32_t tb = tq + (uint32_t)(b * BN);
+                    tmem_ld32(tb + column(0), v[0]);
 #pragma unroll
                     for (int j0 = 0; j0 < C::kCpt; j0 += 32) {
+                        uint32_t(&w)[32] = v[(j0 / 32) & 1];
+                        tmem_ld_wait_for(w);
+                        if (j0 + 32 < C::kCpt) {
+                            tmem_ld32(tb + column(j0 + 32), v[(j0 / 32 + 1) & 1]);
+                        } else {  // the buffer has been read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(tempty_bar(b));
+                        }
                         const bool is_up = kSwiglu && j0 >= C::kCpt / 2;
-                        const int col = kSwiglu ? (is_up ? BN / 2 + half * (C::kCpt / 2) + j0 - C::kCpt / 2
-                                                         : half * (C::kCpt / 2) + j0)
-                                                : half * C::kCpt + j0;
-                        uint32_t v[32];
-                        tmem_ld32(tq + (uint32_t)(b * BN + col), v);
-                        tmem_ld_wait();
-                        if (KIND == PK_WEIGHT_GRAD) {
-                            const float* sc = sb + (size_t)kb * sb_step + c0 + col;
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (c0 + col + j < a.cols) w = __ldg(reinterpret_cast<const float4*>(sc + j));
-                                acc[j0 + j] = fmaf(__uint_as_float(v[j]), s0 * w.x, acc[j0 + j]);
-                                acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), s0 * w.y, acc[j0 + j + 1]);
-                                acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), s0 * w.z, acc[j0 + j + 2]);
-                                acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), s0 * w.w, acc[j0 + j + 3]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                // block boundaries fall on multiples of 16 columns
-                                const float sc = is_up ? ((j0 - C::kCpt / 2 + (j & 16)) < up_cut ? u1 : u2) : s1;
-                                acc[j0 + j] = fmaf(__uint_as_float(v[j]), sc, acc[j0 + j]);
-                            }
+                        for (int j = 0; j < 32; j += 2) {
+                            uint64_t sc = s1;
+                            if (KIND == PK_WEIGHT_GRAD)
+                                sc = mul2(s1, *reinterpret_cast<const uint64_t*>(stage + (j0 + j) * 4));
+                            else if (is_up)  // block boundaries fall on multiples of 16 columns
+                                sc = (j0 - C::kCpt / 2 + (j & 16)) < up_cut ? u1 : u2;
+                            acc2[(j0 + j) / 2] = fma2(pair(w[j], w[j + 1]), sc, acc2[(j0 + j) / 2]);
                         }
                     }
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty_bar(b));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tempty_bar(b));
             }
+            __syncwarp();
+            float acc[C::kCpt];
+#pragma unroll
+            for (int j = 0; j < C::kCpt / 2; ++j) unpair(acc2[j], acc[2 * j], acc[2 * j + 1]);
             if (!ok) break;
             if (ACT == 0) {
                 // ---- rows of the output, 64 bytes at a time
@@ -469,9 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int KIND, int BN, int ACT>
 cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int a_rows, int sms, cudaStream_t s) {
     auto kern = product_kernel<KIND, BN, ACT>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmem);
     if (e != cudaSuccess) return e;
+    if (Cfg<BN>::kMoveRegs) {  // the registers moved between warpgroups must be the block's own
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    }
     const int step = ACT == 1 + MOE_ACT_SWIGLU ? BN / 2 : BN;
     const long long nct = cdiv(a.cols, step);
     const long long rts = KIND == PK_WEIGHT_GRAD ? (long long)a.E * cdiv(a.rows, BM)
