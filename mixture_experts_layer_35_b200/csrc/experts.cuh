@@ -58,6 +58,35 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
         f[4 + i] = b[i];
     }
 }
+// The same eight values as they lie in memory, for code that keeps many of them at once.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const bf16* p) { a = ld_stream16(p); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const { Chunk<bf16>::unpack(a, f); }
+};
+template <>
+struct Raw8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = ld_stream16(p);
+        b = ld_stream16(p + 4);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        float x[4], y[4];
+        Chunk<float>::unpack(a, x);
+        Chunk<float>::unpack(b, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = x[i];
+            f[4 + i] = y[i];
+        }
+    }
+};
 __device__ __forceinline__ void store8(bf16* p, const float (&f)[8]) {
     *reinterpret_cast<uint4*>(p) = Chunk<bf16>::pack(f);
 }

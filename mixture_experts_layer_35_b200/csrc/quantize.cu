@@ -88,16 +88,19 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* __re
     const int kb = blockIdx.x % nk, rest = blockIdx.x / nk, nb = rest % nn, e = rest / nn;
     const int c = kb * kQBlock + (threadIdx.x & 15) * 8, r0 = nb * kQBlock + (threadIdx.x >> 4);
     const size_t base = (size_t)e * N * C;
-    float f[8][8];
+    Raw8<T> v[8];
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-        if (c < C && r0 + 16 * i < N) load8(w + base + (size_t)(r0 + 16 * i) * C + c, f[i]);
+        v[i].zero();
+        if (c < C && r0 + 16 * i < N) v[i].load(w + base + (size_t)(r0 + 16 * i) * C + c);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx = amax8(f[i], mx);
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        v[i].get(f);
+        mx = amax8(f, mx);
+    }
     mx = __reduce_max_sync(0xffffffffu, mx);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
     __syncthreads();
@@ -107,9 +110,12 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* __re
     block_scale(mx, fp8_max(E5M2), scale, factor);
     if (threadIdx.x == 0) scales[blockIdx.x] = scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        v[i].get(f);
         if (c < C && r0 + 16 * i < N)
-            *reinterpret_cast<uint2*>(q + base + (size_t)(r0 + 16 * i) * C + c) = pack8_fp8<E5M2>(f[i], factor);
+            *reinterpret_cast<uint2*>(q + base + (size_t)(r0 + 16 * i) * C + c) = pack8_fp8<E5M2>(f, factor);
+    }
 }
 
 // 128-row blocks inside each expert, 128 columns at a time: as quantize_blocks, but the
@@ -120,48 +126,61 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
                                                                     uint8_t* __restrict__ q,
                                                                     float* __restrict__ scales, int blocks) {
     __shared__ int s_off[MOE_MAX_EXPERTS + 1], s_first[MOE_MAX_EXPERTS + 1], s_warp[33];
-    __shared__ uint32_t s_max[kThreads / 32][kQBlock];
+    __shared__ __align__(16) uint32_t s_max[kThreads / 32][kQBlock];
+    __shared__ __align__(16) float s_factor[kQBlock];
     expert_blocks(offsets, E, P, s_off, s_first, s_warp);
-    const int nc = cdiv(C, kQBlock), lane = threadIdx.x & 31;
+    const int nc = cdiv(C, kQBlock), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int used = min(s_first[E], blocks);
     const int col = (threadIdx.x & 15) * 8, r0 = threadIdx.x >> 4;
     for (long long t = blockIdx.x; t < (long long)used * nc; t += gridDim.x) {
-        const int b = (int)(t / nc), c = (int)(t - (long long)b * nc) * kQBlock + col;
+        const int b = (int)(t / nc), cb = (int)(t - (long long)b * nc) * kQBlock, c = cb + col;
         const int e = expert_of(s_first, E, b, 1);
         const int row0 = s_off[e] + (b - s_first[e]) * kQBlock, have = min(kQBlock, s_off[e + 1] - row0);
-        float f[8][8];
+        Raw8<T> v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-            if (c < C && r0 + 16 * i < have) load8(x + (size_t)(row0 + r0 + 16 * i) * C + c, f[i]);
+            v[i].zero();
+            if (c < C && r0 + 16 * i < have) v[i].load(x + (size_t)(row0 + r0 + 16 * i) * C + c);
         }
-        uint32_t mx[8];
+        uint32_t mx[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            mx[j] = 0;
+        for (int i = 0; i < 8; ++i) {
+            float f[8];
+            v[i].get(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mx[j] = max(mx[j], abs_bits(f[i][j]));
-            mx[j] = max(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-            if (lane < 16) s_max[threadIdx.x >> 5][col + j] = mx[j];
+            for (int j = 0; j < 8; ++j) mx[j] = max(mx[j], abs_bits(f[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx[j] = max(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
+        if (lane < 16) {
+            *reinterpret_cast<uint4*>(&s_max[warp][col]) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+            *reinterpret_cast<uint4*>(&s_max[warp][col + 4]) = make_uint4(mx[4], mx[5], mx[6], mx[7]);
         }
         __syncthreads();
-        float factor[8], scale[8];
+        if (threadIdx.x < kQBlock) {  // one thread per column: its maximum and the two quotients
+            uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) mx[j] = max(mx[j], s_max[i][col + j]);
-            block_scale(mx[j], fp8_max(E5M2), scale[j], factor[j]);
+            for (int i = 0; i < kThreads / 32; ++i) m = max(m, s_max[i][threadIdx.x]);
+            float scale, factor;
+            block_scale(m, fp8_max(E5M2), scale, factor);
+            s_factor[threadIdx.x] = factor;
+            if (cb + (int)threadIdx.x < C) scales[(size_t)b * C + cb + threadIdx.x] = scale;
         }
-        if (r0 == 0 && c < C) store8(scales + (size_t)b * C + c, scale);
+        __syncthreads();
+        float factor[8];
+        const float4 fa = *reinterpret_cast<const float4*>(s_factor + col);
+        const float4 fb = *reinterpret_cast<const float4*>(s_factor + col + 4);
+        factor[0] = fa.x, factor[1] = fa.y, factor[2] = fa.z, factor[3] = fa.w;
+        factor[4] = fb.x, factor[5] = fb.y, factor[6] = fb.z, factor[7] = fb.w;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            float f[8];
+            v[i].get(f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = __fmul_rn(f[i][j], factor[j]);
+            for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], factor[j]);
             if (c < C)
-                *reinterpret_cast<uint2*>(q + ((size_t)b * kQBlock + r0 + 16 * i) * C + c) = pack8_fp8<E5M2>(f[i], 1.0f);
+                *reinterpret_cast<uint2*>(q + ((size_t)b * kQBlock + r0 + 16 * i) * C + c) = pack8_fp8<E5M2>(f, 1.0f);
         }
-        __syncthreads();
     }
 }
 
