@@ -47,51 +47,55 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsArgs a) {
     }
 }
 
-template <typename T, int U, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const RowsArgs a) {
-    constexpr int V = Chunk<T>::V, KU = 8 / U;  // 8 loads in flight per lane
+// Eight loads in flight per lane; the next token's rows and weights are loaded meanwhile.
+template <typename T, bool WEIGHTED>
+__global__ void __launch_bounds__(kThreads, 3) combine_kernel(const RowsArgs a) {
+    constexpr int V = Chunk<T>::V, KU = 8;
     const int lane = threadIdx.x & 31;
-    const int nch = a.H / V, spans = cdiv(nch, 32 * U);
+    const int nch = a.H / V, spans = cdiv(nch, 32);
     const long long n = (long long)a.M * spans, step = (long long)gridDim.x * (kThreads / 32);
     const uint4* ys = static_cast<const uint4*>(a.src);
     uint4* y = static_cast<uint4*>(a.dst);
-    for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < n; i += step) {
-        const int m = (int)(i / spans), c0 = (int)(i - (long long)m * spans) * 32 * U + lane;
-        const int row = slot_row(a, m, lane);
-        const float wt = WEIGHTED && lane < a.K ? a.w[(size_t)m * a.K + lane] : 1.0f;
-        float acc[U][V];
+    long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    int row = -1;
+    float wt = 1.0f;
+    auto load_slots = [&](long long unit) {
+        const int m = (int)(unit / spans);
+        row = slot_row(a, m, lane);
+        if (WEIGHTED && lane < a.K) wt = a.w[(size_t)m * a.K + lane];
+    };
+    if (i < n) load_slots(i);
+    for (; i < n; i += step) {
+        const int m = (int)(i / spans), c = (int)(i - (long long)m * spans) * 32 + lane;
+        const bool in = c < nch;
+        const int row_m = row;
+        const float wt_m = wt;
+        float acc[V];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[u][j] = 0.0f;
+        for (int j = 0; j < V; ++j) acc[j] = 0.0f;
         for (int k0 = 0; k0 < a.K; k0 += KU) {
-            uint4 v[KU][U];
-            int p[KU];
+            uint4 v[KU];
+            uint32_t use = 0;
 #pragma unroll
             for (int kk = 0; kk < KU; ++kk) {
-                p[kk] = __shfl_sync(0xffffffffu, row, (k0 + kk) & 31);
-                if (k0 + kk >= a.K) p[kk] = -1;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (p[kk] >= 0 && c0 + 32 * u < nch) v[kk][u] = ld_stream16(ys + (size_t)p[kk] * nch + c0 + 32 * u);
-            }
-#pragma unroll
-            for (int kk = 0; kk < KU; ++kk) {
-                const float w = __shfl_sync(0xffffffffu, wt, (k0 + kk) & 31);
-                if (p[kk] < 0) continue;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (c0 + 32 * u >= nch) continue;
-                    float f[V];
-                    Chunk<T>::unpack(v[kk][u], f);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) acc[u][j] = WEIGHTED ? fmaf(w, f[j], acc[u][j]) : acc[u][j] + f[j];
+                const int p = __shfl_sync(0xffffffffu, row_m, (k0 + kk) & 31);
+                if (k0 + kk < a.K && p >= 0) {
+                    use |= 1u << kk;
+                    if (in) v[kk] = ld_stream16(ys + (size_t)p * nch + c);
                 }
             }
-        }
+            if (k0 == 0 && i + step < n) load_slots(i + step);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + 32 * u < nch) y[(size_t)m * nch + c0 + 32 * u] = Chunk<T>::pack(acc[u]);
+            for (int kk = 0; kk < KU; ++kk) {
+                const float w = WEIGHTED ? __shfl_sync(0xffffffffu, wt_m, (k0 + kk) & 31) : 1.0f;
+                if (!(use >> kk & 1u)) continue;
+                float f[V];
+                Chunk<T>::unpack(v[kk], f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] = WEIGHTED ? fmaf(w, f[j], acc[j]) : acc[j] + f[j];
+            }
+        }
+        if (in) y[(size_t)m * nch + c] = Chunk<T>::pack(acc);
     }
 }
 
@@ -157,7 +161,7 @@ cudaError_t dispatch_t(const RowsArgs& a, int sms, cudaStream_t s) {
 template <typename T, bool WEIGHTED>
 cudaError_t combine_t(const RowsArgs& a, int sms, cudaStream_t s) {
     const long long n = (long long)a.M * cdiv(a.H / Chunk<T>::V, 32);
-    return launch_k(combine_kernel<T, 1, WEIGHTED>, dim3(grid_for(n, sms, 8)), dim3(kThreads), 0, s, false, a);
+    return launch_k(combine_kernel<T, WEIGHTED>, dim3(grid_for(n, sms, 3)), dim3(kThreads), 0, s, false, a);
 }
 
 }  // namespace
