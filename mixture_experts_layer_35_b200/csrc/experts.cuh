@@ -125,10 +125,11 @@ __device__ __forceinline__ uint2 pack8_fp8(const float (&f)[8], float factor) {
 __device__ __forceinline__ float relu2_nan(float g) { return g > 0.0f ? g * g : (g == g ? 0.0f : g); }
 
 // ---------------------------------------------------------------- rows of each expert
-// Exclusive prefix over the experts of ceil(rows / 128), by the whole CTA (at least 32
+// Exclusive prefix over the experts of ceil(rows / UNIT), by the whole CTA (at least 32
 // threads, a multiple of 32): first[0..E], and off[0..E], the row offsets clamped to [0, P]
 // (no offsets: one expert with all rows).  Rows outside [0, P) are therefore never named,
 // whatever the offsets hold.  s_warp: 33 ints.
+template <int UNIT>
 __device__ __forceinline__ void expert_blocks(const int32_t* offsets, int E, int P, int* off, int* first, int* s_warp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     for (int e = tid; e <= E; e += blockDim.x)
@@ -138,7 +139,7 @@ __device__ __forceinline__ void expert_blocks(const int32_t* offsets, int E, int
     int sum = 0;
     for (int i = 0; i < per; ++i) {
         const int e = tid * per + i;
-        if (e < E) sum += cdiv(max(off[e + 1] - off[e], 0), kQBlock);
+        if (e < E) sum += cdiv(max(off[e + 1] - off[e], 0), UNIT);
     }
     int incl = sum;
 #pragma unroll
@@ -154,7 +155,7 @@ __device__ __forceinline__ void expert_blocks(const int32_t* offsets, int E, int
         const int e = tid * per + i;
         if (e < E) {
             first[e] = run;
-            run += cdiv(max(off[e + 1] - off[e], 0), kQBlock);
+            run += cdiv(max(off[e + 1] - off[e], 0), UNIT);
         }
     }
     if (tid == 0) {
@@ -231,9 +232,9 @@ struct ProductArgs {
 struct ProductMaps {
     CUtensorMap a, b;
 };
-// The tile of a launch: output columns, and rows per TMA box of the A operand.
+// The tile of a launch: output columns (of the weights' rows for a fused activation) and rows.
 struct ProductTile {
-    int bn, a_rows;
+    int bn, rows;
 };
 ProductTile product_tile(int kind, int act, const ProductArgs& a, int sms);
 cudaError_t launch_product(int kind, int act, const ProductTile& t, const ProductArgs& a, const ProductMaps& m,

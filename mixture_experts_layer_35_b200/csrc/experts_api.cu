@@ -73,7 +73,7 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
     const size_t out_bytes = (size_t)P * cols * (act ? 1 : dt_bytes(out_dtype));
     if (overlaps(out, out_bytes, aq, (size_t)P * depth) || overlaps(out, out_bytes, wq, (size_t)E * Wn * C))
         return MOE_ERR_INVALID_ARG;
-    moe_status_t st = too_many_tiles(P / 128 + E, cols);
+    moe_status_t st = too_many_tiles(P / 32 + E, cols);
     if (st != MOE_OK) return st;
     ProductArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -97,8 +97,8 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
     const int sms = sm_count();
     const ProductTile t = product_tile(kind, act, a, sms);
     ProductMaps m;
-    const int w_box = kind == PK_INPUT_GRAD || act == 1 + MOE_ACT_SWIGLU ? 128 : t.bn;
-    if (!bytes_map(&m.a, aq, 2, depth, P, 1, t.a_rows) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
+    const int w_box = kind == PK_INPUT_GRAD ? 128 : (act == 1 + MOE_ACT_SWIGLU ? 64 : t.bn);
+    if (!bytes_map(&m.a, aq, 2, depth, P, 1, t.rows) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
         return MOE_ERR_CUDA;
     return launched(launch_product(kind, act, t, a, m, sms, (cudaStream_t)stream));
 }

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
     __shared__ int s_off[MOE_MAX_EXPERTS + 1], s_first[MOE_MAX_EXPERTS + 1], s_warp[33];
     __shared__ __align__(16) uint32_t s_max[kThreads / 32][kQBlock];
     __shared__ __align__(16) float s_factor[kQBlock];
-    expert_blocks(offsets, E, P, s_off, s_first, s_warp);
+    expert_blocks<kQBlock>(offsets, E, P, s_off, s_first, s_warp);
     const int nc = cdiv(C, kQBlock), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int used = min(s_first[E], blocks);
     const int col = (threadIdx.x & 15) * 8, r0 = threadIdx.x >> 4;
