@@ -121,7 +121,12 @@ __device__ __forceinline__ uint2 pack8_fp8(const float (&f)[8], float factor) {
 }
 
 // ---------------------------------------------------------------- activation
-// As the fused layer's, except that a NaN stays one through ReLU^2.
+// As the fused layer's, except that the quotient is the two-instruction one (off by at most 2
+// units in the last place for divisors up to 2^126; 0 above, where the sigmoid is below 2^-126),
+// and that a NaN stays one through ReLU^2.  The correctly rounded quotient's slow path took
+// 10 us of a 128 x 256 tile of the fused product (250 against 160 us for 10240 rows of 256 experts).
+__device__ __forceinline__ float quick_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float quick_swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 __device__ __forceinline__ float relu2_nan(float g) { return g > 0.0f ? g * g : (g == g ? 0.0f : g); }
 
 // ---------------------------------------------------------------- rows of each expert

@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int f0 = t.c0 + half * kH;
 #pragma unroll
                 for (int j = 0; j < kH; ++j) {
-                    h[j] = kSwiglu ? act_swiglu(acc[j], acc[(kSwiglu ? kH : 0) + j]) : relu2_nan(acc[j]);
+                    h[j] = kSwiglu ? quick_swiglu(acc[j], acc[(kSwiglu ? kH : 0) + j]) : relu2_nan(acc[j]);
                     if (f0 + (j & ~15) < a.cols) mx = max(mx, abs_bits(h[j]));
                 }
                 // Two buffers by tile parity: a warp writes one again only after the other warp's

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
             if (SRC != QS_ROWS && c < a.C) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    f[u][j] = SRC == QS_SWIGLU ? act_swiglu(f[u][j], g[SRC == QS_SWIGLU ? u : 0][j]) : relu2_nan(f[u][j]);
+                    f[u][j] = SRC == QS_SWIGLU ? quick_swiglu(f[u][j], g[SRC == QS_SWIGLU ? u : 0][j]) : relu2_nan(f[u][j]);
             }
             if (!QUANT) {
                 if (c < a.C) store8(static_cast<T*>(a.h) + (size_t)m * a.C + c, f[u]);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const T* 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (SWIGLU) {
-                const float sg = 1.0f / (1.0f + __expf(-g[j]));
+                const float sg = quick_sigmoid(g[j]);
                 const float si = g[j] * sg;
                 dg[j] = d[j] * u[j] * fmaf(si, 1.0f - sg, sg);
                 du[j] = d[j] * si;
