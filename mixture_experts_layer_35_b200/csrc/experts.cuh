@@ -235,7 +235,7 @@ struct ProductArgs {
     float* out_scales;     // fused activation: [P, ceil(I / 128)]
 };
 struct ProductMaps {
-    CUtensorMap a, b;
+    CUtensorMap a, b, out;
 };
 // The tile of a launch: output columns (of the weights' rows for a fused activation) and rows.
 struct ProductTile {

@@ -56,6 +56,19 @@ bool bytes_map(CUtensorMap* m, const void* base, int dim, uint64_t inner, uint64
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Output map [depth][rows][cols]: boxes of 128 bytes by 32 rows, in the 128-byte swizzle.
+bool out_map(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t depth) {
+    EncodeTiledFn enc = get_encode_tiled();
+    if (!enc) return false;
+    const uint64_t el = f32 ? 4 : 2;
+    cuuint64_t dims[3] = {cols, rows, depth};
+    cuuint64_t strides[2] = {cols * el, cols * rows * el};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / el), 32, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 moe_status_t too_many_tiles(long long row_tiles, int cols) {
     return row_tiles * cdiv(cols, 64) > 0x3fffffffLL ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
@@ -100,6 +113,8 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
     const int w_box = kind == PK_INPUT_GRAD ? 128 : (act == 1 + MOE_ACT_SWIGLU ? 64 : t.bn);
     if (!bytes_map(&m.a, aq, 2, depth, P, 1, t.rows) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
         return MOE_ERR_CUDA;
+    if (act) m.out = m.a;  // unused
+    else if (!out_map(&m.out, out, a.out_f32, cols, P, 1)) return MOE_ERR_CUDA;
     return launched(launch_product(kind, act, t, a, m, sms, (cudaStream_t)stream));
 }
 
@@ -317,7 +332,9 @@ moe_status_t moe_product_weight_grad(const void* dyq, const float* dy_scales, in
     const int sms = sm_count();
     const ProductTile t = product_tile(PK_WEIGHT_GRAD, 0, a, sms);
     ProductMaps m;
-    if (!bytes_map(&m.a, dyq, 2, N, rows, 1, 128) || !bytes_map(&m.b, xq, 2, C, rows, 1, 128)) return MOE_ERR_CUDA;
+    if (!bytes_map(&m.a, dyq, 2, N, rows, 1, 128) || !bytes_map(&m.b, xq, 2, C, rows, 1, 128) ||
+        !out_map(&m.out, dw, a.out_f32, C, N, E))
+        return MOE_ERR_CUDA;
     return launched(launch_product(PK_WEIGHT_GRAD, 0, t, a, m, sms, (cudaStream_t)stream));
 }
 

@@ -41,16 +41,18 @@ constexpr int kRegsLaunch = (128 * kRegsIssue + 256 * kRegsEpilogue + kThreads -
 // HT: rows of a tile, 128, or 32 where experts have few rows.  A 32-row tile loads only its
 // rows; the MMA's other 96 lanes read whatever follows them in shared memory, and nothing
 // reads their sums.
-template <int KIND, int BN, int HT>
+template <int KIND, int BN, int HT, int ACT>
 struct Cfg {
     static constexpr int kABytes = HT * BKB;
     static constexpr int kStageBytes = kABytes + BN * BKB;
     static constexpr int kBufs = BN == 256 ? 2 : 4;
     static constexpr int kTmemCols = kBufs * BN;
     static constexpr int kCpt = BN / 2;  // columns of a tile per epilogue thread
-    // Epilogue warps with rows, and each one's staging: 32 rows x 64 bytes.
+    // Epilogue warps with rows, and each one's staging: two boxes of 32 rows x 128 bytes for the
+    // copy engine, or 32 rows x 64 bytes where a tile's rows are few or its values 8-bit.
     static constexpr int kRowWarps = HT == 32 ? 2 : kEpiWarps;
-    static constexpr int kStageOut = 2048;
+    static constexpr bool kBulkStore = HT == 128 && ACT == 0;
+    static constexpr int kStageOut = kBulkStore ? 8192 : 2048;
     // Ring of scales, one slot per block along the contraction: the rows' 128, and the weight
     // blocks' (four for each half of the columns) or, for the weight gradient, the columns'.
     static constexpr int kSlots = 4;
@@ -58,7 +60,7 @@ struct Cfg {
     static constexpr size_t kTables = 512 + (size_t)(2 * (MOE_MAX_EXPERTS + 1) + 34) * 4;
     static constexpr size_t kScales = (kTables + 15) / 16 * 16;
     static constexpr size_t kAmax = kScales + (size_t)kSlots * kSlotFloats * 4;
-    static constexpr size_t kMeta = kAmax + (KIND == PK_FORWARD ? 4 * BM * 4 : 0);
+    static constexpr size_t kMeta = kAmax + (ACT ? 4 * BM * 4 : 0);
     static constexpr int kFit =
         (int)((227 * 1024 - 1024 - kMeta - kRowWarps * kStageOut) / kStageBytes);
     static constexpr int kStages = kFit < 16 ? kFit : 16;
@@ -212,11 +214,33 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, const uint4 (&v)[4], 
     __syncwarp();
 }
 
+// A box of 32 rows x 128 bytes from shared memory to global memory, what lies outside the tensor
+// dropped, or added to what is there.
+__device__ __forceinline__ void store_box(const CUtensorMap* tm, uint32_t src, int c0, int c1, int c2, bool add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(tm)),
+                     "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(tm)),
+                     "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Waits until at most N of this thread's boxes are still being read from shared memory.
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 template <int KIND, int BN, int HT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap tm_a,
-                   const __grid_constant__ CUtensorMap tm_b) {
-    using C = Cfg<KIND, BN, HT>;
+                   const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_out) {
+    using C = Cfg<KIND, BN, HT, ACT>;
     constexpr bool kSwiglu = ACT == 1 + MOE_ACT_SWIGLU;
     constexpr bool kAmn = KIND == PK_WEIGHT_GRAD, kBmn = KIND != PK_FORWARD;
     constexpr int kColStep = kSwiglu ? BN / 2 : BN;  // output columns of a tile
@@ -262,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
+        if (C::kBulkStore) tma_prefetch_desc(&tm_out);
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     expert_blocks<HT>(a.offsets, a.E, a.P, s_off, s_first, s_warp);
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = q * 32 + lane;  // this thread's row of the tile
         uint8_t* stage = staging + (HT == 32 ? half : warp - 4) * C::kStageOut;
         const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * C::kCpt);
-        int it = 0, ntile = 0;
+        int it = 0, ntile = 0, nbox = 0;
         bool ok = true;
         // (the warps without rows of a 32-row tile have nothing to do)
         for (int tile = HT == 32 && q != 0 ? total : blockIdx.x; tile < total; tile += gridDim.x, ++ntile) {
@@ -466,8 +491,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const size_t out_row0 = (KIND == PK_WEIGHT_GRAD ? (size_t)t.e * a.rows : 0) + t.row0 + q * 32;
                 const int c = t.c0 + half * C::kCpt, rows = t.n - q * 32;
                 const bool add = KIND == PK_WEIGHT_GRAD && a.accumulate;
+                if (C::kBulkStore && KIND != PK_WEIGHT_GRAD && rows < 32) {  // staged by hand below
+                    if (lane == 0) store_wait_read<0>();
+                    __syncwarp();
+                }
+                // Whole 32-row blocks go through the copy engine (rows past an expert's end must not be
+                // written; past the tensor's end it drops them), two boxes at a time per warp, so that
+                // they drain while the next tile is summed.
+                const bool boxes = C::kBulkStore && (KIND == PK_WEIGHT_GRAD ? a.out_f32 || !add : rows >= 32);
                 if (!live || (add && t.nk == 0)) {
                     // nothing to write
+                } else if (boxes) {
+                    const int row = t.row0 + q * 32, e = KIND == PK_WEIGHT_GRAD ? t.e : 0;
+                    auto box = [&](int j0, auto chunk) {  // chunk(j): 16 bytes of this thread's row
+                        if (lane == 0) store_wait_read<1>();
+                        __syncwarp();
+                        uint8_t* slot = stage + (nbox & 1) * 4096;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(slot + lane * 128 + ((j ^ (lane & 7)) << 4)) = chunk(j);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) store_box(&tm_out, smem_u32(slot), c + j0, row, e, add);
+                        ++nbox;
+                    };
+                    if (a.out_f32) {
+#pragma unroll
+                        for (int j0 = 0; j0 < C::kCpt; j0 += 32) {
+                            if (c + j0 >= a.cols) break;
+                            box(j0, [&](int j) {
+                                return make_uint4(__float_as_uint(acc[j0 + 4 * j]), __float_as_uint(acc[j0 + 4 * j + 1]),
+                                                  __float_as_uint(acc[j0 + 4 * j + 2]),
+                                                  __float_as_uint(acc[j0 + 4 * j + 3]));
+                            });
+                        }
+                    } else {
+#pragma unroll
+                        for (int j0 = 0; j0 + 64 <= C::kCpt; j0 += 64) {
+                            if (c + j0 >= a.cols) break;
+                            box(j0, [&](int j) {
+                                float f[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) f[i] = acc[j0 + 8 * j + i];
+                                return Chunk<bf16>::pack(f);
+                            });
+                        }
+                    }
                 } else if (a.out_f32 || add) {  // FP32 pieces also where BF16 values are added to: rounded once
 #pragma unroll
                     for (int j0 = 0; j0 < C::kCpt; j0 += 16) {
@@ -562,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (C::kBulkStore && lane == 0) store_wait();
     }
 
     tc_fence_before();
@@ -577,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int KIND, int BN, int HT, int ACT>
 cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s) {
-    using C = Cfg<KIND, BN, HT>;
+    using C = Cfg<KIND, BN, HT, ACT>;
     auto kern = product_kernel<KIND, BN, HT, ACT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
@@ -591,13 +661,13 @@ cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaSt
     const long long nct = cdiv(a.cols, step);
     const long long rts = KIND == PK_WEIGHT_GRAD ? (long long)a.E * cdiv(a.rows, BM) : a.P / HT + std::min(a.E, a.P);
     const int grid = (int)std::max<long long>(1, std::min<long long>(nct * rts, sms));
-    return launch_k(kern, dim3(grid), dim3(kThreads), C::kSmem, s, false, a, m.a, m.b);
+    return launch_k(kern, dim3(grid), dim3(kThreads), C::kSmem, s, false, a, m.a, m.b, m.out);
 }
 
 }  // namespace
 
 ProductTile product_tile(int kind, int act, const ProductArgs& a, int sms) {
-    if (kind == PK_WEIGHT_GRAD) return {256, 128};
+    if (kind == PK_WEIGHT_GRAD) return {(long long)a.blocks >= 6LL * a.E ? 256 : 128, 128};
     const int ht = (long long)a.P >= 32LL * a.E ? 128 : 32;
     if (act) return {act == 1 + MOE_ACT_SWIGLU ? 256 : 128, ht};
     if (ht == 128) return {256, 128};
@@ -613,7 +683,9 @@ cudaError_t launch_product(int kind, int act, const ProductTile& t, const Produc
         return tall ? launch_t<PK_FORWARD, 256, 128, kSw>(a, m, sms, s) : launch_t<PK_FORWARD, 256, 32, kSw>(a, m, sms, s);
     if (act == kRe)
         return tall ? launch_t<PK_FORWARD, 128, 128, kRe>(a, m, sms, s) : launch_t<PK_FORWARD, 128, 32, kRe>(a, m, sms, s);
-    if (kind == PK_WEIGHT_GRAD) return launch_t<PK_WEIGHT_GRAD, 256, 128, 0>(a, m, sms, s);
+    if (kind == PK_WEIGHT_GRAD)
+        return t.bn == 256 ? launch_t<PK_WEIGHT_GRAD, 256, 128, 0>(a, m, sms, s)
+                           : launch_t<PK_WEIGHT_GRAD, 128, 128, 0>(a, m, sms, s);
     if (kind == PK_INPUT_GRAD)
         return tall ? launch_t<PK_INPUT_GRAD, 256, 128, 0>(a, m, sms, s)
                     : launch_t<PK_INPUT_GRAD, 128, 32, 0>(a, m, sms, s);
