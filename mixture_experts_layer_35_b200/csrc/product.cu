@@ -439,21 +439,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float* sc = s_scales + (size_t)i * C::kSlotFloats;
                     const float* sw = sc + BM + (KIND == PK_WEIGHT_GRAD ? half * C::kCpt : 4 * half);
                     const uint32_t tb = tq + (uint32_t)(b * BN);
-                    // 16 columns at a time, the next ones loading while these are added.  (With 32 the
-                    // register allocator copies the loaded values into pairs: 1014 -> 1435 us at 16384 x
-                    // 8192 x 8192.)
-                    uint32_t v[2][16];
-                    tmem_ld16(tb, v[0]);
+                    // Up to 64 columns are read in one go: with few rows two warps of one scheduler do all
+                    // the sums, and each read's latency counts (product of 128 rows of 256 experts: 55 ->
+                    // 50 us).  128 are read 16 at a time, the next ones loading while these are added:
+                    // there are not the registers for more (with 32 the allocator copies the loaded values
+                    // into pairs: 1014 -> 1435 us at 16384 x 8192 x 8192).  So are the weight gradient's 64
+                    // (119 against 127 us for 64 experts x 256 rows x 1024 x 2048).
+                    constexpr bool kAtOnce = C::kCpt <= 64 && KIND != PK_WEIGHT_GRAD;
+                    constexpr int kVec = kAtOnce ? C::kCpt / 16 : 2;
+                    uint32_t v[kVec][16];
+#pragma unroll
+                    for (int i16 = 0; i16 < (kAtOnce ? kVec : 1); ++i16) tmem_ld16(tb + 16 * i16, v[i16]);
                     const float s0 = sc[r];
                     const float s1 = KIND == PK_WEIGHT_GRAD ? s0 : s0 * sw[0];
                     const float u1 = kSwiglu ? s0 * sw[1] : 0.0f, u2 = kSwiglu ? s0 * sw[2] : 0.0f;
 #pragma unroll
                     for (int j0 = 0; j0 < C::kCpt; j0 += 16) {
-                        uint32_t(&w)[16] = v[(j0 / 16) & 1];
+                        uint32_t(&w)[16] = v[(j0 / 16) % kVec];
                         tmem_ld_wait_for(w);
-                        if (j0 + 16 < C::kCpt) {
-                            tmem_ld16(tb + j0 + 16, v[(j0 / 16 + 1) & 1]);
-                        } else {  // the buffer has been read
+                        if (!kAtOnce && j0 + 16 < C::kCpt) tmem_ld16(tb + j0 + 16, v[(j0 / 16 + 1) % kVec]);
+                        if (j0 == (kAtOnce ? 0 : C::kCpt - 16)) {  // the buffer has been read
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(tempty_bar(b));

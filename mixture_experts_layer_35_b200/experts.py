@@ -18,7 +18,6 @@ is launched, and a refusal by the library raises ``moe.MoEError``.  Work and new
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -59,9 +58,9 @@ def _tensor(name: str, t, device, dtypes, shape):
         raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {tuple('any' if n is None else n for n in shape)}, "
-                         f"got {tuple(t.shape)}")
+    got = t.shape
+    if got != shape and (len(got) != len(shape) or any(n is not None and n != m for n, m in zip(shape, got))):
+        raise ValueError(f"{name}: expected shape {tuple('any' if n is None else n for n in shape)}, got {tuple(got)}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if not t.is_contiguous():
@@ -73,7 +72,7 @@ def _first(name: str, t):
     """The device of an operator's first tensor."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
     return t.device
 
@@ -88,28 +87,36 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
+# The current stream's handle without building a torch.cuda.Stream (0.1 against 2.3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """Makes ``device`` current, and ``stream`` when one is given, for the outputs' allocation and the
-    launch; ``ptr`` is the stream's handle."""
+    launch; entering gives the stream's handle."""
+    __slots__ = ("_guards", "_stream", "_device")
 
     def __init__(self, device, stream):
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
-        self._guards = [] if torch.cuda.current_device() == device.index else [torch.cuda.device(device)]
         if stream is not None:
-            self._guards.append(torch.cuda.stream(stream))
-        self._stream, self._device = stream, device
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
+        self._guards, self._stream, self._device = (), stream, device
 
     def __enter__(self):
+        device, stream = self._device, self._stream
+        if stream is not None:
+            self._guards = (torch.cuda.stream(stream),)  # makes its device current too
+        elif torch.cuda.current_device() != device.index:
+            self._guards = (torch.cuda.device(device),)
         for g in self._guards:
             g.__enter__()
-        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._device)
-        return s.cuda_stream
+        return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
     def __exit__(self, *exc):
-        for g in reversed(self._guards):
+        for g in self._guards:
             g.__exit__(*exc)
 
 
