@@ -215,35 +215,39 @@ cudaError_t launch_quantize_columns(const void* x, bool f32, int P, int C, const
 cudaError_t launch_activation_backward(const void* y, const void* dh, bool f32, bool swiglu, int P, int I, void* dy,
                                        int sms, cudaStream_t s);
 
-enum ProductKind { PK_FORWARD = 0, PK_INPUT_GRAD = 1, PK_WEIGHT_GRAD = 2 };
+enum ProductKind { PK_FORWARD = 0, PK_INPUT_GRAD = 1 };
 struct ProductArgs {
-    int rows;              // output rows per group bound: P (forward, input gradient), N (weight gradient)
+    int rows;              // weight gradient: output rows per expert (N)
     int cols;              // output columns: N, C, C; I for a fused activation
-    int depth;             // contraction: C, N; padded rows (weight gradient)
     int P, E;
     int nbl;               // blocks of 128 along the contraction (forward, input gradient)
     int wn, wk;            // weight scale blocks along N and C
     const int32_t* offsets;
-    const float* sa;       // scales of the A operand: [P, nbl], or [blocks, N]
-    const float* sb;       // weight scales [E, wn, wk], or x scales [blocks, C]
+    const float* sa;       // row scales [P, nbl]; weight gradient: dy's [blocks, N]
+    const float* sb;       // weight scales [E, wn, wk]; weight gradient: x's [blocks, C]
     int blocks;            // weight gradient: 128-row blocks in the padded operands (P = 128 * blocks)
-    int a_e5m2, b_e5m2;
+    int a_e5m2, b_e5m2;    // types of the rows (dy); weight gradient: of x
     int out_f32, accumulate;
     int up;                // SwiGLU: row of the first up feature
     int h_e5m2;
     void* out;
     float* out_scales;     // fused activation: [P, ceil(I / 128)]
 };
+// Forward, input gradient: a = rows, b = weights.  Weight gradient: a = dy, b = x, out = dw.
 struct ProductMaps {
     CUtensorMap a, b, out;
 };
-// The tile of a launch: output columns (of the weights' rows for a fused activation) and rows.
-struct ProductTile {
-    int bn, rows;
-};
-ProductTile product_tile(int kind, int act, const ProductArgs& a, int sms);
-cudaError_t launch_product(int kind, int act, const ProductTile& t, const ProductArgs& a, const ProductMaps& m,
-                           int sms, cudaStream_t s);
+// Rows per tile of a forward product or input gradient when its experts have few rows
+// (launch_product_few), or 0 (launch_product).
+int product_few_rows(int act, const ProductArgs& a);
+constexpr int kFewBoxRows = 32;  // rows per TMA box of the row operand there (128 in launch_product)
+cudaError_t launch_product(int kind, int act, const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s);
+cudaError_t launch_product_few(int kind, int act, int tile_rows, const ProductArgs& a, const ProductMaps& m, int sms,
+                               cudaStream_t s);
+cudaError_t launch_weight_grad(const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s);
+// Error words, read and cleared (product_error takes the others' in).
+cudaError_t product_few_error(int* code, cudaStream_t s);
+cudaError_t weight_grad_error(int* code, cudaStream_t s);
 cudaError_t product_error(int* code, cudaStream_t s);
 
 }  // namespace moe

@@ -90,9 +90,7 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
     if (st != MOE_OK) return st;
     ProductArgs a;
     std::memset(&a, 0, sizeof(a));
-    a.rows = P;
     a.cols = cols;
-    a.depth = depth;
     a.P = P;
     a.E = E;
     a.nbl = cdiv(depth, kQBlock);
@@ -108,14 +106,15 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
     a.out = out;
     a.out_scales = out_scales;
     const int sms = sm_count();
-    const ProductTile t = product_tile(kind, act, a, sms);
+    const int few = product_few_rows(act, a);
+    const int w_box = few || kind == PK_INPUT_GRAD ? 128 : (act == 0 ? 256 : (act == 1 + MOE_ACT_SWIGLU ? 64 : 128));
     ProductMaps m;
-    const int w_box = kind == PK_INPUT_GRAD ? 128 : (act == 1 + MOE_ACT_SWIGLU ? 64 : t.bn);
-    if (!bytes_map(&m.a, aq, 2, depth, P, 1, t.rows) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
+    if (!bytes_map(&m.a, aq, 2, depth, P, 1, few ? kFewBoxRows : 128) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
         return MOE_ERR_CUDA;
+    if (few) return launched(launch_product_few(kind, act, few, a, m, sms, (cudaStream_t)stream));
     if (act) m.out = m.a;  // unused
     else if (!out_map(&m.out, out, a.out_f32, cols, P, 1)) return MOE_ERR_CUDA;
-    return launched(launch_product(kind, act, t, a, m, sms, (cudaStream_t)stream));
+    return launched(launch_product(kind, act, a, m, sms, (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -330,12 +329,11 @@ moe_status_t moe_product_weight_grad(const void* dyq, const float* dy_scales, in
     a.accumulate = accumulate;
     a.out = dw;
     const int sms = sm_count();
-    const ProductTile t = product_tile(PK_WEIGHT_GRAD, 0, a, sms);
     ProductMaps m;
     if (!bytes_map(&m.a, dyq, 2, N, rows, 1, 128) || !bytes_map(&m.b, xq, 2, C, rows, 1, 128) ||
         !out_map(&m.out, dw, a.out_f32, C, N, E))
         return MOE_ERR_CUDA;
-    return launched(launch_product(PK_WEIGHT_GRAD, 0, t, a, m, sms, (cudaStream_t)stream));
+    return launched(launch_weight_grad(a, m, sms, (cudaStream_t)stream));
 }
 
 moe_status_t moe_product_get_error(int* code, void* stream) {
