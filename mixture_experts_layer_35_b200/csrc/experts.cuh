@@ -11,6 +11,14 @@ namespace moe {
 constexpr int kQBlock = 128;         // columns or rows that share one scale
 constexpr float kAmaxFloor = 0x1p-96f;  // smallest block maximum a scale is made from
 
+// The operators' kernels are launched so that each may start while the kernel before it in the
+// stream drains.  Called before the first access to global memory: waits until that kernel is
+// complete, and lets the next one start its own prologue.
+__device__ __forceinline__ void chain() {
+    pdl_wait();
+    pdl_trigger();
+}
+
 // ---------------------------------------------------------------- 16-byte chunks of a row
 template <typename T>
 struct Chunk;  // V values of T in 16 bytes, as FP32

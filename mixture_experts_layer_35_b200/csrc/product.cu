@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (ACT == 0) tma_prefetch_desc(&tm_out);
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    chain();
     expert_blocks<BM>(a.offsets, a.E, a.P, s_off, s_first, s_warp);
     tc_fence_before();
     __syncthreads();
@@ -440,6 +441,8 @@ cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaSt
     using C = Cfg<BN, ACT>;
     const cudaError_t e = prepare_product(product_kernel<KIND, BN, ACT>, C::kSmem, C::kMoveRegs);
     if (e != cudaSuccess) return e;
+    // (without the overlap with the kernel before that the other operators have: 270 against 264 us for
+    // the input gradient of 24576 rows of 128 experts x 1856 x 2688)
     const int step = ACT == 1 + MOE_ACT_SWIGLU ? BN / 2 : BN;
     const long long tiles = (long long)cdiv(a.cols, step) * (a.P / BM + std::min(a.E, a.P));
     return launch_k(product_kernel<KIND, BN, ACT>, dim3((unsigned)std::min<long long>(tiles, sms)),

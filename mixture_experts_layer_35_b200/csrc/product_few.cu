@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma_prefetch_desc(&tm_x);
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    chain();
     expert_blocks<NT>(a.offsets, a.E, a.P, s_off, s_first, s_warp);
     tc_fence_before();
     __syncthreads();
@@ -455,7 +456,7 @@ cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaSt
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)cdiv(a.cols, BF) * (a.P / NT + std::min(a.E, a.P));
     return launch_k(few_kernel<KIND, NT, ACT>, dim3((unsigned)std::min<long long>(tiles, sms)),
-                    dim3(kProductThreads), C::kSmem, s, false, a, m.b, m.a);
+                    dim3(kProductThreads), C::kSmem, s, true, a, m.b, m.a);
 }
 template <int KIND, int ACT>
 cudaError_t launch_rows(const ProductArgs& a, const ProductMaps& m, int rows, int sms, cudaStream_t s) {

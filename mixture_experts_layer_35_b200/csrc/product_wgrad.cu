@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma_prefetch_desc(&tm_out);
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    chain();
     expert_blocks<kQBlock>(a.offsets, a.E, a.P, s_off, s_first, s_warp);
     tc_fence_before();
     __syncthreads();
@@ -342,8 +343,7 @@ cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaSt
     const cudaError_t e = prepare_product(wgrad_kernel<BN>, C::kSmem, C::kMoveRegs);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.E * cdiv(a.rows, BM) * cdiv(a.cols, BN);
-    return launch_k(wgrad_kernel<BN>, dim3((unsigned)std::min<long long>(tiles, sms)), dim3(kProductThreads), C::kSmem, s,
-                    false, a, m.a, m.b, m.out);
+    return launch_k(wgrad_kernel<BN>, dim3((unsigned)std::min<long long>(tiles, sms)), dim3(kProductThreads), C::kSmem, s, true, a, m.a, m.b, m.out);
 }
 
 }  // namespace

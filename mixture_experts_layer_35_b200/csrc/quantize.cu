@@ -25,6 +25,7 @@ __device__ __forceinline__ uint32_t amax8(const float (&f)[8], uint32_t m) {
 // blocks of a row, U times.
 template <typename T, int SRC, bool QUANT, bool E5M2, int U>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
+    chain();
     const int lane = threadIdx.x & 31, sub = lane >> 4;
     const int nb = cdiv(a.C, kQBlock), spans = cdiv(nb, 2 * U);
     const int ld = SRC == QS_SWIGLU ? 2 * a.C : a.C;
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* __re
                                                                    uint8_t* __restrict__ q,
                                                                    float* __restrict__ scales) {
     __shared__ uint32_t s_max[kThreads / 32];
+    chain();
     const int nk = cdiv(C, kQBlock), nn = cdiv(N, kQBlock);
     const int kb = blockIdx.x % nk, rest = blockIdx.x / nk, nb = rest % nn, e = rest / nn;
     const int c = kb * kQBlock + (threadIdx.x & 15) * 8, r0 = nb * kQBlock + (threadIdx.x >> 4);
@@ -128,6 +130,7 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
     __shared__ int s_off[MOE_MAX_EXPERTS + 1], s_first[MOE_MAX_EXPERTS + 1], s_warp[33];
     __shared__ __align__(16) uint32_t s_max[kThreads / 32][kQBlock];
     __shared__ __align__(16) float s_factor[kQBlock];
+    chain();
     expert_blocks<kQBlock>(offsets, E, P, s_off, s_first, s_warp);
     const int nc = cdiv(C, kQBlock), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int used = min(s_first[E], blocks);
@@ -190,6 +193,7 @@ template <typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const T* __restrict__ y,
                                                                        const T* __restrict__ dh, int P, int I,
                                                                        T* __restrict__ dy) {
+    chain();
     const int nch = I / 8, ld = SWIGLU ? 2 * I : I;
     const long long n = (long long)P * nch, step = (long long)gridDim.x * kThreads;
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
@@ -225,10 +229,10 @@ cudaError_t rows_t(const QuantArgs& a, int sms, cudaStream_t s) {
     const long long warps = (long long)a.M * cdiv(nb, 4);
     if (warps >= 8LL * sms)
         return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 2>, dim3(grid_for((warps + 7) / 8, sms, 8)),
-                        dim3(kThreads), 0, s, false, a);
+                        dim3(kThreads), 0, s, true, a);
     const long long w1 = (long long)a.M * cdiv(nb, 2);
     return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 1>, dim3(grid_for((w1 + 7) / 8, sms, 8)), dim3(kThreads),
-                    0, s, false, a);
+                    0, s, true, a);
 }
 template <typename T, int SRC>
 cudaError_t rows_src(const QuantArgs& a, int sms, cudaStream_t s) {
@@ -246,14 +250,14 @@ template <typename T>
 cudaError_t blocks_t(const void* w, int E, int N, int C, int e5m2, uint8_t* q, float* scales, cudaStream_t s) {
     const dim3 grid((unsigned)(E * cdiv(N, kQBlock) * cdiv(C, kQBlock)));
     auto kern = e5m2 ? quantize_blocks_kernel<T, true> : quantize_blocks_kernel<T, false>;
-    return launch_k(kern, grid, dim3(kThreads), 0, s, false, static_cast<const T*>(w), N, C, q, scales);
+    return launch_k(kern, grid, dim3(kThreads), 0, s, true, static_cast<const T*>(w), N, C, q, scales);
 }
 template <typename T>
 cudaError_t columns_t(const void* x, int P, int C, const int32_t* offsets, int E, int e5m2, uint8_t* q, float* scales,
                       int blocks, int sms, cudaStream_t s) {
     const long long tiles = (long long)std::min(blocks, P / kQBlock + std::min(E, P)) * cdiv(C, kQBlock);
     auto kern = e5m2 ? quantize_columns_kernel<T, true> : quantize_columns_kernel<T, false>;
-    return launch_k(kern, dim3(grid_for(tiles, sms, 4)), dim3(kThreads), 0, s, false, static_cast<const T*>(x), P, C,
+    return launch_k(kern, dim3(grid_for(tiles, sms, 4)), dim3(kThreads), 0, s, true, static_cast<const T*>(x), P, C,
                     offsets, E, q, scales, blocks);
 }
 template <typename T>
@@ -261,7 +265,7 @@ cudaError_t act_backward_t(const void* y, const void* dh, bool swiglu, int P, in
                            cudaStream_t s) {
     const long long n = (long long)P * (I / 8);
     auto kern = swiglu ? activation_backward_kernel<T, true> : activation_backward_kernel<T, false>;
-    return launch_k(kern, dim3(grid_for((n + kThreads - 1) / kThreads, sms, 8)), dim3(kThreads), 0, s, false,
+    return launch_k(kern, dim3(grid_for((n + kThreads - 1) / kThreads, sms, 8)), dim3(kThreads), 0, s, true,
                     static_cast<const T*>(y), static_cast<const T*>(dh), P, I, static_cast<T*>(dy));
 }
 

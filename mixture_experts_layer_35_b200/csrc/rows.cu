@@ -25,6 +25,7 @@ __device__ __forceinline__ int slot_row(const RowsArgs& a, int m, int lane) {
 
 template <typename T, int U>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsArgs a) {
+    chain();
     const int lane = threadIdx.x & 31;
     const int nch = a.H / Chunk<T>::V, spans = cdiv(nch, 32 * U);
     const long long n = (long long)a.M * spans, step = (long long)gridDim.x * (kThreads / 32);
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsArgs a) {
 // Eight loads in flight per lane; the next token's rows and weights are loaded meanwhile.
 template <typename T, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads, 3) combine_kernel(const RowsArgs a) {
+    chain();
     constexpr int V = Chunk<T>::V, KU = 8;
     const int lane = threadIdx.x & 31;
     const int nch = a.H / V, spans = cdiv(nch, 32);
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 3) combine_kernel(const RowsArgs a) 
 // from memory once and from L1 by the other slots' warps of the block.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowsArgs a) {
+    chain();
     constexpr int V = Chunk<T>::V, U = 4;
     const int lane = threadIdx.x & 31;
     const int nch = a.H / V;
@@ -154,14 +157,13 @@ cudaError_t dispatch_t(const RowsArgs& a, int sms, cudaStream_t s) {
     const int nch = a.H / Chunk<T>::V;
     if ((long long)a.M * cdiv(nch, 128) >= 8LL * sms)
         return launch_k(dispatch_kernel<T, 4>, dim3(grid_for((long long)a.M * cdiv(nch, 128), sms, 8)), dim3(kThreads),
-                        0, s, false, a);
-    return launch_k(dispatch_kernel<T, 1>, dim3(grid_for((long long)a.M * cdiv(nch, 32), sms, 8)), dim3(kThreads), 0, s,
-                    false, a);
+                        0, s, true, a);
+    return launch_k(dispatch_kernel<T, 1>, dim3(grid_for((long long)a.M * cdiv(nch, 32), sms, 8)), dim3(kThreads), 0, s, true, a);
 }
 template <typename T, bool WEIGHTED>
 cudaError_t combine_t(const RowsArgs& a, int sms, cudaStream_t s) {
     const long long n = (long long)a.M * cdiv(a.H / Chunk<T>::V, 32);
-    return launch_k(combine_kernel<T, WEIGHTED>, dim3(grid_for(n, sms, 3)), dim3(kThreads), 0, s, false, a);
+    return launch_k(combine_kernel<T, WEIGHTED>, dim3(grid_for(n, sms, 3)), dim3(kThreads), 0, s, true, a);
 }
 
 }  // namespace
@@ -175,8 +177,8 @@ cudaError_t launch_combine(const RowsArgs& a, bool f32, int sms, cudaStream_t s)
 }
 cudaError_t launch_combine_backward(const RowsArgs& a, bool f32, int sms, cudaStream_t s) {
     const int grid = grid_for((long long)a.M * a.K, sms, 8);
-    if (f32) return launch_k(combine_backward_kernel<float>, dim3(grid), dim3(kThreads), 0, s, false, a);
-    return launch_k(combine_backward_kernel<bf16>, dim3(grid), dim3(kThreads), 0, s, false, a);
+    if (f32) return launch_k(combine_backward_kernel<float>, dim3(grid), dim3(kThreads), 0, s, true, a);
+    return launch_k(combine_backward_kernel<bf16>, dim3(grid), dim3(kThreads), 0, s, true, a);
 }
 
 }  // namespace moe
