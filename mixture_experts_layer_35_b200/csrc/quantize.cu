@@ -39,39 +39,45 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
             row = lane < a.K ? a.inv[(size_t)lane * a.M + m] : -1;
             if ((unsigned)row >= (unsigned)a.P) row = -1;
         }
-        float f[U][8], g[SRC == QS_SWIGLU ? U : 1][8];
+        Raw8<T> v[U], w[SRC == QS_SWIGLU ? U : 1];  // as they lie: all loads in flight at once
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = (b0 + 2 * u) * kQBlock + (lane & 15) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[u][j] = 0.0f;
+            v[u].zero();
+            if (SRC == QS_SWIGLU) w[SRC == QS_SWIGLU ? u : 0].zero();
             if (c < a.C) {
-                load8(src + (size_t)m * ld + c, f[u]);
-                if (SRC == QS_SWIGLU) load8(src + (size_t)m * ld + a.C + c, g[SRC == QS_SWIGLU ? u : 0]);
+                v[u].load(src + (size_t)m * ld + c);
+                if (SRC == QS_SWIGLU) w[SRC == QS_SWIGLU ? u : 0].load(src + (size_t)m * ld + a.C + c);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int b = b0 + 2 * u, c = b * kQBlock + (lane & 15) * 8;
-            if (SRC != QS_ROWS && c < a.C) {
+            float f[8];
+            v[u].get(f);
+            if (SRC == QS_SWIGLU) {
+                float g[8];
+                w[SRC == QS_SWIGLU ? u : 0].get(g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[u][j] = SRC == QS_SWIGLU ? quick_swiglu(f[u][j], g[SRC == QS_SWIGLU ? u : 0][j]) : relu2_nan(f[u][j]);
+                for (int j = 0; j < 8; ++j) f[j] = quick_swiglu(f[j], g[j]);
+            } else if (SRC == QS_RELU2) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = relu2_nan(f[j]);
             }
             if (!QUANT) {
-                if (c < a.C) store8(static_cast<T*>(a.h) + (size_t)m * a.C + c, f[u]);
+                if (c < a.C) store8(static_cast<T*>(a.h) + (size_t)m * a.C + c, f);
                 continue;
             }
-            uint32_t mx = amax8(f[u], 0u);
+            uint32_t mx = amax8(f, 0u);
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             float scale, factor;
             block_scale(mx, fmax, scale, factor);
-            const uint2 v = pack8_fp8<E5M2>(f[u], factor);
+            const uint2 out = pack8_fp8<E5M2>(f, factor);
             for (int k = 0; k < a.K; ++k) {
                 const int p = a.inv ? __shfl_sync(0xffffffffu, row, k) : m;
                 if (p < 0) continue;
-                if (c < a.C) *reinterpret_cast<uint2*>(a.q + (size_t)p * a.C + c) = v;
+                if (c < a.C) *reinterpret_cast<uint2*>(a.q + (size_t)p * a.C + c) = out;
                 if ((lane & 15) == 0 && b < nb) a.scales[(size_t)p * nb + b] = scale;
             }
         }
@@ -195,10 +201,12 @@ __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const T* 
                                                                        T* __restrict__ dy) {
     chain();
     const int nch = I / 8, ld = SWIGLU ? 2 * I : I;
-    const long long n = (long long)P * nch, step = (long long)gridDim.x * kThreads;
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-        const long long p = i / nch;
-        const int c = (int)(i - p * nch) * 8;
+    // This thread's chunks of eight, as (row, chunk) pairs advanced without a division.
+    const long long first = (long long)blockIdx.x * kThreads + threadIdx.x, step = (long long)gridDim.x * kThreads;
+    const int step_p = (int)(step / nch), step_c = (int)(step - (long long)step_p * nch) * 8;
+    size_t p = (size_t)(first / nch);
+    int c = (int)(first - (long long)p * nch) * 8;
+    for (; p < (size_t)P; p += step_p) {
         float g[8], u[8], d[8], dg[8], du[8];
         load8(y + p * ld + c, g);
         if (SWIGLU) load8(y + p * ld + I + c, u);
@@ -216,6 +224,11 @@ __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const T* 
         }
         store8(dy + p * ld + c, dg);
         if (SWIGLU) store8(dy + p * ld + I + c, du);
+        c += step_c;
+        if (c >= I) {
+            c -= I;
+            ++p;
+        }
     }
 }
 
@@ -226,12 +239,20 @@ int grid_for(long long blocks, int sms, int per_sm) {
 template <typename T, int SRC, bool QUANT, bool E5M2>
 cudaError_t rows_t(const QuantArgs& a, int sms, cudaStream_t s) {
     const int nb = cdiv(a.C, kQBlock);
-    const long long warps = (long long)a.M * cdiv(nb, 4);
-    if (warps >= 8LL * sms)
-        return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 2>, dim3(grid_for((warps + 7) / 8, sms, 8)),
-                        dim3(kThreads), 0, s, true, a);
-    const long long w1 = (long long)a.M * cdiv(nb, 2);
-    return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 1>, dim3(grid_for((w1 + 7) / 8, sms, 8)), dim3(kThreads),
+    // Blocks per warp: with four (two halves of a warp) enough bytes are in flight; eight for plain
+    // rows written once (32768 x 2048: 50 -> 44 us; rows written to K places go slower, 51 -> 53, and
+    // SwiGLU's two operands are eight loads already, 18 -> 31); two while there are few warps.
+    const long long pairs = (long long)a.M * cdiv(nb, 2);
+    const bool once = SRC != QS_SWIGLU && !a.inv;
+    if constexpr (SRC != QS_SWIGLU) {
+        if (once && pairs >= 32LL * sms)
+            return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 4>,
+                            dim3(grid_for(((long long)a.M * cdiv(nb, 8) + 7) / 8, sms, 16)), dim3(kThreads), 0, s, true, a);
+    }
+    if (pairs >= 16LL * sms)
+        return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 2>,
+                        dim3(grid_for(((long long)a.M * cdiv(nb, 4) + 7) / 8, sms, 16)), dim3(kThreads), 0, s, true, a);
+    return launch_k(quantize_rows_kernel<T, SRC, QUANT, E5M2, 1>, dim3(grid_for((pairs + 7) / 8, sms, 16)), dim3(kThreads),
                     0, s, true, a);
 }
 template <typename T, int SRC>
@@ -265,7 +286,7 @@ cudaError_t act_backward_t(const void* y, const void* dh, bool swiglu, int P, in
                            cudaStream_t s) {
     const long long n = (long long)P * (I / 8);
     auto kern = swiglu ? activation_backward_kernel<T, true> : activation_backward_kernel<T, false>;
-    return launch_k(kern, dim3(grid_for((n + kThreads - 1) / kThreads, sms, 8)), dim3(kThreads), 0, s, true,
+    return launch_k(kern, dim3(grid_for((n + kThreads - 1) / kThreads, sms, 16)), dim3(kThreads), 0, s, true,
                     static_cast<const T*>(y), static_cast<const T*>(dh), P, I, static_cast<T*>(dy));
 }
 

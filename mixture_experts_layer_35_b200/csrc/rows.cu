@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowsArgs a) {
 
 // Eight loads in flight per lane; the next token's rows and weights are loaded meanwhile.
 template <typename T, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads, 3) combine_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) combine_kernel(const RowsArgs a) {
     chain();
     constexpr int V = Chunk<T>::V, KU = 8;
     const int lane = threadIdx.x & 31;
@@ -156,14 +156,14 @@ template <typename T>
 cudaError_t dispatch_t(const RowsArgs& a, int sms, cudaStream_t s) {
     const int nch = a.H / Chunk<T>::V;
     if ((long long)a.M * cdiv(nch, 128) >= 8LL * sms)
-        return launch_k(dispatch_kernel<T, 4>, dim3(grid_for((long long)a.M * cdiv(nch, 128), sms, 8)), dim3(kThreads),
+        return launch_k(dispatch_kernel<T, 4>, dim3(grid_for((long long)a.M * cdiv(nch, 128), sms, 32)), dim3(kThreads),
                         0, s, true, a);
     return launch_k(dispatch_kernel<T, 1>, dim3(grid_for((long long)a.M * cdiv(nch, 32), sms, 8)), dim3(kThreads), 0, s, true, a);
 }
 template <typename T, bool WEIGHTED>
 cudaError_t combine_t(const RowsArgs& a, int sms, cudaStream_t s) {
     const long long n = (long long)a.M * cdiv(a.H / Chunk<T>::V, 32);
-    return launch_k(combine_kernel<T, WEIGHTED>, dim3(grid_for(n, sms, 3)), dim3(kThreads), 0, s, true, a);
+    return launch_k(combine_kernel<T, WEIGHTED>, dim3(grid_for(n, sms, 4)), dim3(kThreads), 0, s, true, a);
 }
 
 }  // namespace
