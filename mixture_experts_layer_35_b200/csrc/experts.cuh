@@ -248,7 +248,7 @@ struct ProductMaps {
 // Rows per tile of a forward product or input gradient when its experts have few rows
 // (launch_product_few), or 0 (launch_product).
 int product_few_rows(int act, const ProductArgs& a);
-constexpr int kFewBoxRows = 32;  // rows per TMA box of the row operand there (128 in launch_product)
+constexpr int kRowBox = 32;  // rows per TMA box of the row operand
 cudaError_t launch_product(int kind, int act, const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s);
 cudaError_t launch_product_few(int kind, int act, int tile_rows, const ProductArgs& a, const ProductMaps& m, int sms,
                                cudaStream_t s);

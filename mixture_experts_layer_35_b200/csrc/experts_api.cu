@@ -109,7 +109,7 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
     const int few = product_few_rows(act, a);
     const int w_box = few || kind == PK_INPUT_GRAD ? 128 : (act == 0 ? 256 : (act == 1 + MOE_ACT_SWIGLU ? 64 : 128));
     ProductMaps m;
-    if (!bytes_map(&m.a, aq, 2, depth, P, 1, few ? kFewBoxRows : 128) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
+    if (!bytes_map(&m.a, aq, 2, depth, P, 1, kRowBox) || !bytes_map(&m.b, wq, 3, C, Wn, E, w_box))
         return MOE_ERR_CUDA;
     if (few) return launched(launch_product_few(kind, act, few, a, m, sms, (cudaStream_t)stream));
     if (act) m.out = m.a;  // unused

@@ -159,7 +159,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         const uint32_t sa = base_u32 + (uint32_t)s * C::kStageBytes, sb = sa + C::kABytes;
                         const uint32_t bar = full_bar(s);
                         mbar_expect_tx(bar, C::kStageBytes);
-                        tma_load_2d(sa, &tm_a, bar, kb * BKB, t.row0);
+                        // Boxes of 32 rows; those past the expert's rows are zeros from behind the tensor's
+                        // end, which move no bytes (266 -> 264 us, 24576 rows of 128 experts x 1856 x 2688).
+                        for (int j = 0; j < BM / 32; ++j)
+                            tma_load_2d(sa + (uint32_t)(32 * j * BKB), &tm_a, bar, kb * BKB,
+                                        32 * j < t.n ? t.row0 + 32 * j : a.P);
                         if (KIND == PK_INPUT_GRAD) {
                             for (int j = 0; j < BN / 128; ++j)
                                 tma_load_3d(sb + j * 16384, &tm_b, bar, t.c0 + j * 128, kb * BKB, t.e);

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 bool ok = true;
                 for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
                     const Tile t = tile_at(tile);
-                    const int boxes = cdiv(t.n, kFewBoxRows);
+                    const int boxes = cdiv(t.n, kRowBox);
                     auto load_w = [&](uint32_t dst, uint32_t bar, int c0, int c1) {
                         if (t.alone) tma_load_3d_hint(dst, &tm_w, bar, c0, c1, t.e, once);
                         else tma_load_3d(dst, &tm_w, bar, c0, c1, t.e);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         }
                         const uint32_t sw = base_u32 + (uint32_t)s * C::kStageBytes, sx = sw + C::kNA * A_BYTES;
                         const uint32_t bar = full_bar(s);
-                        mbar_expect_tx(bar, (uint32_t)(C::kNA * A_BYTES + boxes * kFewBoxRows * BKB));
+                        mbar_expect_tx(bar, (uint32_t)(C::kNA * A_BYTES + boxes * kRowBox * BKB));
                         if (KIND == PK_INPUT_GRAD) {
                             load_w(sw, bar, t.f0, kb * BKB);
                         } else {
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                             if (kSwiglu) load_w(sw + A_BYTES, bar, kb * BKB, a.up + t.f0);
                         }
                         for (int j = 0; j < boxes; ++j)
-                            tma_load_2d(sx + (uint32_t)(j * kFewBoxRows * BKB), &tm_x, bar, kb * BKB,
-                                        t.row0 + j * kFewBoxRows);
+                            tma_load_2d(sx + (uint32_t)(j * kRowBox * BKB), &tm_x, bar, kb * BKB,
+                                        t.row0 + j * kRowBox);
                     }
                 }
             }
