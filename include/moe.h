@@ -26,7 +26,8 @@
  *     is launched and the status says why.  T == 0 (moe_fused_forward) and M == 0
  *     (moe_router_topk) return MOE_OK and launch nothing.
  *   - There is no hidden global state: concurrent calls are safe when they use distinct
- *     outputs and workspaces.
+ *     outputs and workspaces.  (Two error words per device collect what went wrong: the static
+ *     scratch's, moe_noalloc_get_error, and the products', moe_product_get_error.)
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
