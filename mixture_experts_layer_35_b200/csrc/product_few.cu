@@ -9,6 +9,11 @@
 // read them as broadcasts.  Those reads compete with the tensor cores' for shared memory: at 256 rows per
 // expert this orientation takes 437 us where product.cu's takes 193 (256 experts x 1024 x 2048).
 // At 8 rows it takes 57 us where product.cu's takes 64 (128 experts; 4.7 TB/s of weights).
+//
+// A call with fewer tiles than half of the SMs (one token, a few experts) splits the contraction
+// over a cluster of two CTAs: each sums its half of the blocks, the second writes its FP32 sums into
+// the first one's shared memory, and that one adds them.  One token of top-8, H 2048, I 512:
+// forward 10.8 -> 9.9 us, SwiGLU 14.0 -> 11.8 (clusters of four: 9.9 and 11.5).
 #include "product.cuh"
 
 namespace moe {
@@ -18,8 +23,57 @@ __device__ int g_few_error;  // MOE_DEVERR_* bits of these products on this devi
 
 constexpr int BF = 128;  // features of a tile
 constexpr int A_BYTES = BF * BKB;
+constexpr int kSplit = 2;  // CTAs that share a tile's contraction
 
-template <int NT, int ACT>
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster, whatever has happened in it: no wait can stay open.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Address of `addr` in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait for arrivals and data of other CTAs of the cluster; bounded in the same way.
+__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    const uint64_t t0 = globaltimer_ns();
+    uint32_t n = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((++n & 255u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                set_dev_error(err, MOE_DEVERR_WAIT_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+template <int NT, int ACT, bool SPLIT>
 struct Cfg {
     static constexpr bool kSwiglu = ACT == 1 + MOE_ACT_SWIGLU;
     static constexpr int kNA = kSwiglu ? 2 : 1;  // weight tiles: gate and up
@@ -41,12 +95,15 @@ struct Cfg {
     static constexpr size_t kAmax = kScales + (size_t)kSlots * kSlotFloats * 4;  // [tile parity][quarter][NT]
     static constexpr size_t kFactor = kAmax + (ACT ? 8 * NT * 4 : 0);            // [warp][kHalf]
     static constexpr size_t kMeta = kFactor + (ACT ? kEpiWarps * kHalf * 4 : 0);
-    static constexpr int kFit = (int)((227 * 1024 - 1024 - kMeta) / kStageBytes);
+    // The second CTA's sums: [value][epilogue thread].
+    static constexpr int kValues = kNA * kGroups * 16;
+    static constexpr int kPartBytes = SPLIT ? kValues * 32 * kEpiWarps * 4 : 0;
+    static constexpr int kFit = (int)((227 * 1024 - 1024 - kMeta - kPartBytes) / kStageBytes);
     static constexpr int kStages = kFit < 16 ? kFit : 16;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kMeta;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kPartBytes + kMeta;
     static_assert(kAccCols <= 256, "two accumulator buffers must fit");
     static_assert(kStages >= 3, "ring too shallow");
-    static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 2) + 8 <= 512, "barrier block");
+    static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 3) + 8 <= 512, "barrier block");
 };
 
 struct Tile {
@@ -70,17 +127,18 @@ __device__ __forceinline__ Tile decode(const ProductArgs& a, const int* off, con
     return t;
 }
 
-template <int KIND, int NT, int ACT>
+template <int KIND, int NT, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kProductThreads, 1)
     few_kernel(const ProductArgs a, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_x) {
-    using C = Cfg<NT, ACT>;
+    using C = Cfg<NT, ACT, SPLIT>;
     constexpr bool kSwiglu = C::kSwiglu;
     constexpr bool kAmn = KIND == PK_INPUT_GRAD;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
-    uint8_t* meta = smem_raw + (base_u32 - raw_u32) + (size_t)C::kStages * C::kStageBytes;
+    float* parts = reinterpret_cast<float*>(smem_raw + (base_u32 - raw_u32) + (size_t)C::kStages * C::kStageBytes);
+    uint8_t* meta = reinterpret_cast<uint8_t*>(parts) + C::kPartBytes;
     const uint32_t bar_u32 = smem_u32(meta);
     auto full_bar = [&](int s) { return bar_u32 + 8u * s; };
     auto empty_bar = [&](int s) { return bar_u32 + 8u * (C::kStages + s); };
@@ -89,7 +147,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     auto sfull_bar = [&](int i) { return bar_u32 + 8u * (2 * C::kStages + 2 * C::kBufs + i); };
     auto sempty_bar = [&](int i) { return bar_u32 + 8u * (2 * C::kStages + 2 * C::kBufs + C::kSlots + i); };
     auto amax_bar = [&](int h) { return bar_u32 + 8u * (2 * C::kStages + 2 * C::kBufs + 2 * C::kSlots + h); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * C::kStages + 2 * C::kBufs + 2 * C::kSlots + 2));
+    const uint32_t part_bar = amax_bar(2);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * C::kStages + 2 * C::kBufs + 2 * C::kSlots + 3));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_off = reinterpret_cast<int*>(meta + 512);
     int* s_first = s_off + MOE_MAX_EXPERTS + 1;
@@ -98,6 +157,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int* err = &g_few_error;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = SPLIT ? (int)cluster_rank() : 0;
+    constexpr int split = SPLIT ? kSplit : 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(full_bar(s), 1);
@@ -112,6 +173,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             mbar_init(sempty_bar(i), kEpiWarps);
         }
         for (int h = 0; h < 2; ++h) mbar_init(amax_bar(h), 4);
+        if (SPLIT) mbar_init(part_bar, 32 * kEpiWarps);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_w);
@@ -122,9 +184,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     expert_blocks<NT>(a.offsets, a.E, a.P, s_off, s_first, s_warp);
     tc_fence_before();
     __syncthreads();
+    if (SPLIT) cluster_sync();  // every CTA of the cluster has its barriers
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int nft = cdiv(a.cols, BF), nk = a.nbl;
+    // This CTA's blocks of the contraction, its first tile, and the tiles apart from it.  (A split
+    // call has at least as many clusters as tiles: one tile each.)
+    const int kb0 = SPLIT ? nk * rank / split : 0, kb1 = SPLIT ? nk * (rank + 1) / split : nk;
+    const int tile0 = SPLIT ? (int)blockIdx.x / split : (int)blockIdx.x, tile_step = (int)gridDim.x / split;
     const int total = s_first[a.E] * nft;
     auto tile_at = [&](int tile) { return decode<NT>(a, s_off, s_first, nft, tile); };
 
@@ -136,14 +203,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const uint64_t once = l2_policy_evict_first();
                 int it = 0;
                 bool ok = true;
-                for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+                for (int tile = tile0; ok && tile < total; tile += tile_step) {
                     const Tile t = tile_at(tile);
                     const int boxes = cdiv(t.n, kRowBox);
                     auto load_w = [&](uint32_t dst, uint32_t bar, int c0, int c1) {
                         if (t.alone) tma_load_3d_hint(dst, &tm_w, bar, c0, c1, t.e, once);
                         else tma_load_3d(dst, &tm_w, bar, c0, c1, t.e);
                     };
-                    for (int kb = 0; kb < nk; ++kb, ++it) {
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         const int s = it % C::kStages;
                         if (!mbar_wait(empty_bar(s), ((uint32_t)(it / C::kStages) & 1u) ^ 1u, abort_flag, err)) {
                             ok = false;
@@ -169,10 +236,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if (lane == 0) {
                 int it = 0;
                 bool ok = true;
-                for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+                for (int tile = tile0; ok && tile < total; tile += tile_step) {
                     const Tile t = tile_at(tile);
                     const uint32_t idesc = idesc_fp8(0, a.a_e5m2, kAmn, 0, cdiv(t.n, 16) * 16);
-                    for (int kb = 0; kb < nk; ++kb, ++it) {
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         const int s = it % C::kStages, b = it % C::kBufs;
                         if (!mbar_wait(full_bar(s), (uint32_t)(it / C::kStages) & 1u, abort_flag, err) ||
                             !mbar_wait(tempty_bar(b), ((uint32_t)(it / C::kBufs) & 1u) ^ 1u, abort_flag, err)) {
@@ -230,19 +297,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     up0 = we + (size_t)min(u, a.wn - 1) * a.wk;
                     up1 = we + (size_t)min(u + 1, a.wn - 1) * a.wk;
                 }
-                load(0);
+                load(kb0);
             };
             int it = 0;
             bool ok = true;
-            if ((int)blockIdx.x < total) begin_tile(blockIdx.x);
-            for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-                for (int kb = 0; kb < nk; ++kb, ++it) {
+            if (tile0 < total) begin_tile(tile0);
+            for (int tile = tile0; ok && tile < total; tile += tile_step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int i = it % C::kSlots;
                     float now[kMine], wn[3] = {w[0], w[1], w[2]};
 #pragma unroll
                     for (int k = 0; k < kMine; ++k) now[k] = x[k];
-                    if (kb + 1 < nk) load(kb + 1);
-                    else if (tile + (int)gridDim.x < total) begin_tile(tile + gridDim.x);
+                    if (kb + 1 < kb1) load(kb + 1);
+                    else if (tile + tile_step < total) begin_tile(tile + tile_step);
                     if (!mbar_wait(sempty_bar(i), ((uint32_t)(it / C::kSlots) & 1u) ^ 1u, abort_flag, err)) {
                         ok = false;
                         break;
@@ -269,7 +336,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(16 * half);
         int it = 0, ntile = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++ntile) {
+        for (int tile = tile0; tile < total; tile += tile_step, ++ntile) {
             const Tile t = tile_at(tile);
             const int f = t.f0 + q * 32 + lane;  // this thread's feature
             const bool live = t.f0 + q * 32 < a.cols;
@@ -281,7 +348,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int p = 0; p < C::kNA * C::kGroups; ++p)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) acc2[p][j] = 0;
-            for (int kb = 0; kb < nk; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int b = it % C::kBufs, i = it % C::kSlots;
                 if (!mbar_wait(sfull_bar(i), (uint32_t)(it / C::kSlots) & 1u, abort_flag, err) ||
                     !mbar_wait(tfull_bar(b), (uint32_t)(it / C::kBufs) & 1u, abort_flag, err)) {
@@ -332,6 +399,35 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (lane == 0) mbar_arrive(sempty_bar(i));
             }
             if (!ok) break;
+            if (SPLIT && rank > 0) {  // this CTA's sums to the first one's shared memory
+                const uint32_t mine = smem_u32(parts + threadIdx.x - 128);
+                const uint32_t dst = peer_smem(mine, 0);
+#pragma unroll
+                for (int p = 0; p < C::kNA * C::kGroups; ++p)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float x, y;
+                        unpair(acc2[p][j], x, y);
+                        peer_store(dst + (16 * p + 2 * j) * (32 * kEpiWarps * 4), x);
+                        peer_store(dst + (16 * p + 2 * j + 1) * (32 * kEpiWarps * 4), y);
+                    }
+                peer_arrive(peer_smem(part_bar, 0));
+                continue;
+            }
+            if (SPLIT) {  // the second CTA's sums
+                if (!cluster_wait(part_bar, (uint32_t)ntile & 1u, abort_flag, err)) break;
+                const float* from = parts + threadIdx.x - 128;
+#pragma unroll
+                for (int p = 0; p < C::kNA * C::kGroups; ++p)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float x, y;
+                        unpair(acc2[p][j], x, y);
+                        x += from[(16 * p + 2 * j) * 32 * kEpiWarps];
+                        y += from[(16 * p + 2 * j + 1) * 32 * kEpiWarps];
+                        acc2[p][j] = pair(x, y);
+                    }
+            }
             if (ACT == 0) {
                 // ---- a warp holds 32 neighbouring features of each row: FP32 rows are written as they
                 // are, 128 bytes each; for BF16 two lanes swap halves of two rows, so that each
@@ -447,20 +543,41 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     }
     if (warp == 1) tmem_dealloc(tmem_base, C::kTmemCols);
+    if (SPLIT) cluster_sync();  // no CTA leaves while another may still write to it
 }
 
-template <int KIND, int NT, int ACT>
+template <int KIND, int NT, int ACT, bool SPLIT>
 cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s) {
-    using C = Cfg<NT, ACT>;
-    const cudaError_t e = prepare_product(few_kernel<KIND, NT, ACT>, C::kSmem, C::kMoveRegs);
+    using C = Cfg<NT, ACT, SPLIT>;
+    auto kern = few_kernel<KIND, NT, ACT, SPLIT>;
+    const cudaError_t e = prepare_product(kern, C::kSmem, C::kMoveRegs);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)cdiv(a.cols, BF) * (a.P / NT + std::min(a.E, a.P));
-    return launch_k(few_kernel<KIND, NT, ACT>, dim3((unsigned)std::min<long long>(tiles, sms)),
-                    dim3(kProductThreads), C::kSmem, s, true, a, m.b, m.a);
+    if constexpr (!SPLIT)
+        return launch_k(kern, dim3((unsigned)std::min<long long>(tiles, sms)), dim3(kProductThreads), C::kSmem, s, true, a,
+                        m.b, m.a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles * kSplit);
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kSplit;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, m.b, m.a);
 }
 template <int KIND, int ACT>
 cudaError_t launch_rows(const ProductArgs& a, const ProductMaps& m, int rows, int sms, cudaStream_t s) {
-    return rows == 32 ? launch_t<KIND, 32, ACT>(a, m, sms, s) : launch_t<KIND, 64, ACT>(a, m, sms, s);
+    if (rows != 32) return launch_t<KIND, 64, ACT, false>(a, m, sms, s);
+    const long long tiles = (long long)cdiv(a.cols, BF) * (a.P / 32 + std::min(a.E, a.P));
+    if (kSplit * tiles <= sms && a.nbl >= 2 * kSplit) return launch_t<KIND, 32, ACT, true>(a, m, sms, s);
+    return launch_t<KIND, 32, ACT, false>(a, m, sms, s);
 }
 
 }  // namespace
