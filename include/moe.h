@@ -372,7 +372,7 @@ moe_status_t moe_quantize_blocks(const void* w, int dtype, int E, int N, int C, 
  * moe_product_weight_grad.  Each expert's rows start a new block; its last block is filled
  * up with zero rows.  x [P, C]; with B = moe_column_blocks(P, E): q [B * 128, C] and
  * scales [B, C], of which the sum over experts of ceil(rows / 128) blocks is written and the
- * rest left as it was. */
+ * rest left as it was; without offsets all B are written, a block without rows as zeros. */
 int moe_column_blocks(int P, int E);
 moe_status_t moe_quantize_columns(const void* x, int dtype, int P, int C, const int32_t* offsets, int E, int fp8,
                                   void* q, float* scales, void* stream);

@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
     chain();
     expert_blocks<kQBlock>(offsets, E, P, s_off, s_first, s_warp);
     const int nc = cdiv(C, kQBlock), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int used = min(s_first[E], blocks);
+    // Without offsets every block is the one expert's: one that P leaves empty is written as zero rows.
+    const int used = offsets ? min(s_first[E], blocks) : blocks;
     const int col = (threadIdx.x & 15) * 8, r0 = threadIdx.x >> 4;
     for (long long t = blockIdx.x; t < (long long)used * nc; t += gridDim.x) {
         const int b = (int)(t / nc), cb = (int)(t - (long long)b * nc) * kQBlock, c = cb + col;

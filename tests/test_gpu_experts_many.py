@@ -87,3 +87,29 @@ def test_weight_gradient(counts, out, accumulate):
     T.assert_within(dw, want, T.sum_bound(mag, max(-(-n // 128) for n in counts) + 1) +
                     want.abs() * T.HALF[out] * 1.01)
     assert ex.get_error() == 0
+
+
+@pytest.mark.parametrize("P", [1, 127, 128, 256, 300])
+def test_one_expert_without_offsets(P):
+    """All blocks are the expert's then, the one that P leaves empty too: what lay in the buffers before
+    (here NaN) must not reach the weight gradient."""
+    N, C = 144, 272
+    g = T.gen(P)
+    dy, x = T.randn((P, N), g, BF), T.randn((P, C), g, BF)
+    B = ex.column_blocks(P, 1)
+
+    def room(cols):
+        return (torch.full((B * 128, cols), 0x7f, dtype=torch.uint8, device="cuda").view(T.E4),
+                torch.full((B, cols), float("nan"), device="cuda"))
+
+    d, xq = ex.quantize_columns(dy, out=room(N)), ex.quantize_columns(x, out=room(C))
+    dw = ex.product_weight_grad(*d, *xq)
+    off = T.offsets([P])
+    want = ex.product_weight_grad(*ex.quantize_columns(dy, off, out=room(N)), *ex.quantize_columns(x, off, out=room(C)), off)
+    assert torch.equal(dw, want) and not dw.isnan().any()
+    w = ex.quantize_blocks(T.randn((1, N, C), g))
+    q = ex.quantize_rows(x)
+    assert torch.equal(ex.product(*q, *w), ex.product(*q, *w, off))
+    assert torch.equal(ex.product_input_grad(*ex.quantize_rows(dy), *w), ex.product_input_grad(*ex.quantize_rows(dy), *w, off))
+    a, b = ex.product_activation(*q, *w, act="relu2"), ex.product_activation(*q, *w, off, "relu2")
+    assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
