@@ -320,8 +320,8 @@ moe_status_t moe_get_error(void* ws, int* code, void* stream);
  *
  * Rows sorted by expert: P rows, expert e's at [offsets[e], offsets[e + 1]).
  * `offsets` [E + 1] int32 as moe_permute writes them, or NULL for one expert (E == 1) with
- * all P rows.  Values are clamped to [0, P]; rows from offsets[E] on are not read, and
- * are left as they were in the outputs.  Limits: P <= MOE_MAX_ROWS, E <= MOE_MAX_EXPERTS,
+ * all P rows.  Values are clamped to [0, P], and one below its predecessor to that; rows from
+ * offsets[E] on are not read, and are left as they were in the outputs.  Limits: P <= MOE_MAX_ROWS, E <= MOE_MAX_EXPERTS,
  * every feature count <= MOE_MAX_FEATURES.
  * ---------------------------------------------------------------------------------- */
 #define MOE_MAX_ROWS (MOE_MAX_TOKENS * 8)

@@ -138,22 +138,34 @@ __device__ __forceinline__ float quick_swiglu(float g, float u) { return __fdivi
 __device__ __forceinline__ float relu2_nan(float g) { return g > 0.0f ? g * g : (g == g ? 0.0f : g); }
 
 // ---------------------------------------------------------------- rows of each expert
-// Exclusive prefix over the experts of ceil(rows / UNIT), by the whole CTA (at least 32
-// threads, a multiple of 32): first[0..E], and off[0..E], the row offsets clamped to [0, P]
-// (no offsets: one expert with all rows).  Rows outside [0, P) are therefore never named,
-// whatever the offsets hold.  s_warp: 33 ints.
+// off[0..E]: the row offsets, clamped to [0, P] and to the largest one before (no offsets: one
+// expert with all rows), so that whatever they hold, experts' rows lie in [0, P), do not overlap and
+// are at most P.  first[0..E]: exclusive prefix over the experts of ceil(rows / UNIT).  By the whole
+// CTA (a multiple of 32 threads); s_warp: 33 ints.
 template <int UNIT>
 __device__ __forceinline__ void expert_blocks(const int32_t* offsets, int E, int P, int* off, int* first, int* s_warp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    for (int e = tid; e <= E; e += blockDim.x)
-        off[e] = offsets ? min(max(offsets[e], 0), P) : (e ? P : 0);
-    __syncthreads();
-    const int per = cdiv(E, (int)blockDim.x);
-    int sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = tid * per + i;
-        if (e < E) sum += cdiv(max(off[e + 1] - off[e], 0), UNIT);
+    const int per = cdiv(E, (int)blockDim.x), e0 = min(tid * per, E), e1 = min(e0 + per, E);  // this thread's experts
+    int top = offsets ? min(max(offsets[0], 0), P) : 0;
+    if (tid == 0) off[0] = top;
+    for (int e = e0; e < e1; ++e) {
+        top = max(top, offsets ? min(offsets[e + 1], P) : P);
+        off[e + 1] = top;
     }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, n);
+    }
+    if (lane == 31) s_warp[warp] = top;
+    top = __shfl_up_sync(0xffffffffu, top, 1);  // the largest of the lanes before
+    if (lane == 0) top = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) top = max(top, s_warp[w]);
+    for (int e = e0; e < e1; ++e) off[e + 1] = max(off[e + 1], top);
+    __syncthreads();
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += cdiv(off[e + 1] - off[e], UNIT);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -164,12 +176,9 @@ __device__ __forceinline__ void expert_blocks(const int32_t* offsets, int E, int
     __syncthreads();
     int run = incl - sum;
     for (int w = 0; w < warp; ++w) run += s_warp[w];
-    for (int i = 0; i < per; ++i) {
-        const int e = tid * per + i;
-        if (e < E) {
-            first[e] = run;
-            run += cdiv(max(off[e + 1] - off[e], 0), UNIT);
-        }
+    for (int e = e0; e < e1; ++e) {
+        first[e] = run;
+        run += cdiv(off[e + 1] - off[e], UNIT);
     }
     if (tid == 0) {
         int total = 0;

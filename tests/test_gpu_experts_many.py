@@ -113,3 +113,34 @@ def test_one_expert_without_offsets(P):
     assert torch.equal(ex.product_input_grad(*ex.quantize_rows(dy), *w), ex.product_input_grad(*ex.quantize_rows(dy), *w, off))
     a, b = ex.product_activation(*q, *w, act="relu2"), ex.product_activation(*q, *w, off, "relu2")
     assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("E", [1, 2, 31, 257, 1000, 1024])
+def test_any_offsets_give_disjoint_rows(E):
+    """Offsets that are no prefix sums act as their running maximum, clamped to the rows there are."""
+    g = T.gen(E)
+    P, N, C = 500, 32, 144
+    raw = torch.randint(-200, 900, (E + 1,), generator=g, device="cuda")
+    raw[::3] = torch.randint(0, P, raw[::3].shape, generator=g, device="cuda")
+    raw = (raw // max(1, 8 - E)).int() if E < 8 else raw.int()
+    good = raw.clamp(0, P).long().cummax(0).values.int()
+    w = ex.quantize_blocks(T.randn((E, N, C), g))
+    q = ex.quantize_rows(T.randn((P, C), g))
+    a, b = (torch.full((P, N), 7.0, dtype=BF, device="cuda") for _ in range(2))
+    ex.product(*q, *w, raw, out=a)
+    ex.product(*q, *w, good, out=b)
+    assert torch.equal(a, b) and (a[:int(good[0])] == 7.0).all() and (a[int(good[-1]):] == 7.0).all()
+    x, dy = T.randn((P, C), g), T.randn((P, N), g)
+    B = ex.column_blocks(P, E)
+
+    def columns(t, off):
+        out = torch.zeros((B * 128, t.shape[1]), dtype=torch.uint8, device="cuda").view(T.E4), \
+            torch.zeros((B, t.shape[1]), device="cuda")
+        return ex.quantize_columns(t, off, out=out)
+
+    for t in (x, dy):
+        c, d = columns(t, raw), columns(t, good)
+        assert torch.equal(c[0].view(torch.uint8), d[0].view(torch.uint8)) and torch.equal(c[1], d[1])
+    assert torch.equal(ex.product_weight_grad(*columns(dy, raw), *columns(x, raw), raw),
+                       ex.product_weight_grad(*columns(dy, good), *columns(x, good), good))
+    assert ex.get_error() == 0
