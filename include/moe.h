@@ -372,7 +372,9 @@ moe_status_t moe_quantize_blocks(const void* w, int dtype, int E, int N, int C, 
  * moe_product_weight_grad.  Each expert's rows start a new block; its last block is filled
  * up with zero rows.  x [P, C]; with B = moe_column_blocks(P, E): q [B * 128, C] and
  * scales [B, C], of which the sum over experts of ceil(rows / 128) blocks is written and the
- * rest left as it was; without offsets all B are written, a block without rows as zeros. */
+ * rest left as it was; without offsets all B are written.  Offsets that reach past P (a row limit)
+ * name blocks whose rows are not there: as far as they lie within the B, they are written too.  A
+ * block without rows is zeros, its scales as well. */
 int moe_column_blocks(int P, int E);
 moe_status_t moe_quantize_columns(const void* x, int dtype, int P, int C, const int32_t* offsets, int E, int fp8,
                                   void* q, float* scales, void* stream);
@@ -410,8 +412,9 @@ moe_status_t moe_product_input_grad(const void* dyq, const float* dy_scales, int
                                     int out_dtype, void* dx, void* stream);
 /* Gradient of moe_product's weights, dw[e, n, c] = sum over the rows p of e of dy[p, n] x[p, c]:
  * dyq [B * 128, N], xq [B * 128, C] and their scales [B, N], [B, C] as moe_quantize_columns
- * writes them with the same offsets (without offsets, all B blocks are the one expert's).  dw [E, N, C] of out_dtype; accumulate 1: added to dw (in FP32, rounded
- * once), 0: written, zeros for an expert without rows. */
+ * writes them with the same offsets and B (without offsets, all B blocks are the one expert's; rows
+ * that offsets name past the P that were quantised count as zero).  dw [E, N, C] of out_dtype;
+ * accumulate 1: added to dw (in FP32, rounded once), 0: written, zeros for an expert without rows. */
 moe_status_t moe_product_weight_grad(const void* dyq, const float* dy_scales, int dy_fp8, const void* xq,
                                      const float* x_scales, int x_fp8, int B, int N, int C, const int32_t* offsets,
                                      int E, int out_dtype, int accumulate, void* dw, void* stream);

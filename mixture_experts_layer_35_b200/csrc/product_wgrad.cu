@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     chain();
+    // Offsets clamped to the room for rows, a.P = 128 * blocks, as the column quantiser lays its blocks out.
     expert_blocks<kQBlock>(a.offsets, a.E, a.P, s_off, s_first, s_warp);
     tc_fence_before();
     __syncthreads();

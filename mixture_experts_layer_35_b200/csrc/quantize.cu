@@ -127,7 +127,10 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* __re
 }
 
 // 128-row blocks inside each expert, 128 columns at a time: as quantize_blocks, but the
-// maximum is one per column, and rows past the expert's end are written as zeros.
+// maximum is one per column, and rows past the expert's end are written as zeros.  Offsets may reach
+// past the P rows (a row limit).  The weight gradient, which reads these blocks, knows the room for
+// them alone and not P, so the blocks are laid out by offsets clamped to the room here too, and one whose
+// rows are all missing is written as zeros, its scales as well.
 template <typename T, bool E5M2>
 __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __restrict__ x, int P, int C,
                                                                     const int32_t* __restrict__ offsets, int E,
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
     __shared__ __align__(16) uint32_t s_max[kThreads / 32][kQBlock];
     __shared__ __align__(16) float s_factor[kQBlock];
     chain();
-    expert_blocks<kQBlock>(offsets, E, P, s_off, s_first, s_warp);
+    expert_blocks<kQBlock>(offsets, E, offsets ? blocks * kQBlock : P, s_off, s_first, s_warp);
     const int nc = cdiv(C, kQBlock), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // Without offsets every block is the one expert's: one that P leaves empty is written as zero rows.
     const int used = offsets ? min(s_first[E], blocks) : blocks;
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
     for (long long t = blockIdx.x; t < (long long)used * nc; t += gridDim.x) {
         const int b = (int)(t / nc), cb = (int)(t - (long long)b * nc) * kQBlock, c = cb + col;
         const int e = expert_of(s_first, E, b, 1);
-        const int row0 = s_off[e] + (b - s_first[e]) * kQBlock, have = min(kQBlock, s_off[e + 1] - row0);
+        const int row0 = s_off[e] + (b - s_first[e]) * kQBlock, have = min(kQBlock, min(s_off[e + 1], P) - row0);
         Raw8<T> v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) quantize_columns_kernel(const T* __r
             float scale, factor;
             block_scale(m, fp8_max(E5M2), scale, factor);
             s_factor[threadIdx.x] = factor;
-            if (cb + (int)threadIdx.x < C) scales[(size_t)b * C + cb + threadIdx.x] = scale;
+            if (cb + (int)threadIdx.x < C) scales[(size_t)b * C + cb + threadIdx.x] = have > 0 ? scale : 0.0f;
         }
         __syncthreads();
         float factor[8];

@@ -277,7 +277,8 @@ def quantize_columns(x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                      dtype: torch.dtype = torch.float8_e4m3fn, out=None, stream=None):
     """[P, C] to 8 bits with one scale per column and 128 rows of an expert (moe_quantize_columns):
     ([B * 128, C] of ``dtype``, [B, C] FP32) with B = column_blocks(P, E); blocks behind the last
-    expert's are left as they were (without offsets: zero rows)."""
+    expert's are left as they were (without offsets: zeros).  Offsets may name more rows than the P
+    that there are: blocks of rows that are not there are zeros."""
     dev = _first("x", x)
     _tensor("x", x, dev, DTYPES, (None, None))
     fp8 = _key(FP8, dtype, "dtype")
