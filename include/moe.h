@@ -313,10 +313,10 @@ moe_status_t moe_get_error(void* ws, int* code, void* stream);
  *   moe_router_topk -> moe_permute -> moe_dispatch_quantize -> moe_product_activation
  *   -> moe_product -> moe_combine.
  * They take no workspace.  Calls on different streams are safe when their outputs are
- * distinct.  Outputs must not overlap inputs.  Zero rows are valid and launch nothing
- * (except where an output of zeros is due: moe_combine without kept slots, and
- * moe_product_weight_grad without rows).  `dtype` is MOE_DT_BF16 or MOE_DT_FP32, `fp8`
- * MOE_DT_E4M3 or MOE_DT_E5M2.
+ * distinct.  An output must not overlap an input or another output, and is refused where it does.
+ * Zero rows are valid and launch nothing (except where an output of zeros is due: moe_combine
+ * without kept slots, and moe_product_weight_grad without rows).  `dtype` is MOE_DT_BF16 or
+ * MOE_DT_FP32, `fp8` MOE_DT_E4M3 or MOE_DT_E5M2.
  *
  * Rows sorted by expert: P rows, expert e's at [offsets[e], offsets[e + 1]).
  * `offsets` [E + 1] int32 as moe_permute writes them, or NULL for one expert (E == 1) with

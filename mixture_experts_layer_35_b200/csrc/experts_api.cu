@@ -1,6 +1,7 @@
 // experts_api.cu -- the C ABI of the expert operators: host-side validation, tensor maps and
 // launches.  Nothing here allocates or synchronises (except moe_product_get_error).
 #include <cstring>
+#include <initializer_list>
 
 #include "experts.cuh"
 
@@ -13,10 +14,28 @@ bool bad_opt(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u)
 bool bad_dtype(int t) { return t != MOE_DT_BF16 && t != MOE_DT_FP32; }
 bool bad_fp8(int t) { return t != MOE_DT_E4M3 && t != MOE_DT_E5M2; }
 size_t dt_bytes(int t) { return t == MOE_DT_FP32 ? 4 : 2; }
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
+// A buffer's bytes; null: not given.
+struct Span {
+    const void* p;
+    size_t n;
+};
+bool overlaps(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
 }
+// An output that shares memory with an input or with another output.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span* p = outs.begin(); p != o; ++p)
+            if (overlaps(*o, *p)) return true;
+        for (const Span& i : ins)
+            if (overlaps(*o, i)) return true;
+    }
+    return false;
+}
+size_t scale_bytes(size_t rows, int cols) { return rows * cdiv(cols, kQBlock) * sizeof(float); }
+size_t slot_bytes(int M, int K) { return (size_t)M * K * 4; }  // inv, weights
+size_t offset_bytes(int E) { return ((size_t)E + 1) * sizeof(int32_t); }
 int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
@@ -84,7 +103,12 @@ moe_status_t run_rows_product(int kind, int act, const void* aq, const float* a_
         return MOE_ERR_INVALID_ARG;
     const int depth = kind == PK_FORWARD ? C : N, cols = kind == PK_FORWARD ? N : C;
     const size_t out_bytes = (size_t)P * cols * (act ? 1 : dt_bytes(out_dtype));
-    if (overlaps(out, out_bytes, aq, (size_t)P * depth) || overlaps(out, out_bytes, wq, (size_t)E * Wn * C))
+    if (clash({{out, out_bytes}, {out_scales, scale_bytes(P, cols)}},
+              {{aq, (size_t)P * depth},
+               {a_scales, scale_bytes(P, depth)},
+               {wq, (size_t)E * Wn * C},
+               {w_scales, scale_bytes((size_t)E * cdiv(Wn, kQBlock), C)},
+               {offsets, offset_bytes(E)}}))
         return MOE_ERR_INVALID_ARG;
     moe_status_t st = too_many_tiles(P / 32 + E, cols);
     if (st != MOE_OK) return st;
@@ -127,7 +151,8 @@ moe_status_t moe_dispatch(const void* x, int dtype, int M, int K, int H, const i
     if (st != MOE_OK) return st;
     if (M == 0 || P == 0) return MOE_OK;
     if (bad_ptr(x) || bad_ptr(inv) || bad_ptr(xs)) return MOE_ERR_INVALID_ARG;
-    if (overlaps(x, (size_t)M * H * dt_bytes(dtype), xs, (size_t)P * H * dt_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    const size_t el = dt_bytes(dtype);
+    if (clash({{xs, (size_t)P * H * el}}, {{x, (size_t)M * H * el}, {inv, slot_bytes(M, K)}})) return MOE_ERR_INVALID_ARG;
     const RowsArgs a = {x, nullptr, inv, nullptr, xs, nullptr, M, K, H, P};
     return launched(launch_dispatch(a, dtype == MOE_DT_FP32, sm_count(), (cudaStream_t)stream));
 }
@@ -138,7 +163,10 @@ moe_status_t moe_combine(const void* ys, int dtype, int M, int K, int H, const i
     if (st != MOE_OK) return st;
     if (M == 0) return MOE_OK;
     if ((P > 0 && bad_ptr(ys)) || bad_ptr(inv) || bad_opt(weights) || bad_ptr(y)) return MOE_ERR_INVALID_ARG;
-    if (overlaps(y, (size_t)M * H * dt_bytes(dtype), ys, (size_t)P * H * dt_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    const size_t el = dt_bytes(dtype);
+    if (clash({{y, (size_t)M * H * el}},
+              {{ys, (size_t)P * H * el}, {inv, slot_bytes(M, K)}, {weights, slot_bytes(M, K)}}))
+        return MOE_ERR_INVALID_ARG;
     const RowsArgs a = {ys, nullptr, inv, weights, y, nullptr, M, K, H, P};
     return launched(launch_combine(a, dtype == MOE_DT_FP32, sm_count(), (cudaStream_t)stream));
 }
@@ -152,7 +180,9 @@ moe_status_t moe_combine_backward(const void* dy, const void* ys, int dtype, int
         bad_ptr(dweights))
         return MOE_ERR_INVALID_ARG;
     const size_t el = dt_bytes(dtype), rows = (size_t)P * H * el;
-    if (overlaps(dys, rows, dy, (size_t)M * H * el) || overlaps(dys, rows, ys, rows)) return MOE_ERR_INVALID_ARG;
+    if (clash({{dys, rows}, {dweights, slot_bytes(M, K)}},
+              {{dy, (size_t)M * H * el}, {ys, rows}, {inv, slot_bytes(M, K)}, {weights, slot_bytes(M, K)}}))
+        return MOE_ERR_INVALID_ARG;
     const RowsArgs a = {ys, dy, inv, weights, dys, dweights, M, K, H, P};
     return launched(launch_combine_backward(a, dtype == MOE_DT_FP32, sm_count(), (cudaStream_t)stream));
 }
@@ -164,7 +194,8 @@ moe_status_t moe_quantize_rows(const void* x, int dtype, int R, int C, int fp8, 
     if (st != MOE_OK) return st;
     if (R == 0) return MOE_OK;
     if (bad_ptr(x) || bad_ptr(q) || bad_ptr(scales)) return MOE_ERR_INVALID_ARG;
-    if (overlaps(x, (size_t)R * C * dt_bytes(dtype), q, (size_t)R * C)) return MOE_ERR_INVALID_ARG;
+    const size_t n = (size_t)R * C;
+    if (clash({{q, n}, {scales, scale_bytes(R, C)}}, {{x, n * dt_bytes(dtype)}})) return MOE_ERR_INVALID_ARG;
     const QuantArgs a = {x, nullptr, static_cast<uint8_t*>(q), scales, nullptr, R, 1, C, R, fp8 == MOE_DT_E5M2};
     return launched(launch_quantize_rows(a, QS_ROWS, dtype == MOE_DT_FP32, sm_count(), (cudaStream_t)stream));
 }
@@ -176,7 +207,9 @@ moe_status_t moe_dispatch_quantize(const void* x, int dtype, int M, int K, int H
     if (bad_fp8(fp8)) return MOE_ERR_INVALID_ARG;
     if (M == 0 || P == 0) return MOE_OK;
     if (bad_ptr(x) || bad_ptr(inv) || bad_ptr(q) || bad_ptr(scales)) return MOE_ERR_INVALID_ARG;
-    if (overlaps(x, (size_t)M * H * dt_bytes(dtype), q, (size_t)P * H)) return MOE_ERR_INVALID_ARG;
+    if (clash({{q, (size_t)P * H}, {scales, scale_bytes(P, H)}},
+              {{x, (size_t)M * H * dt_bytes(dtype)}, {inv, slot_bytes(M, K)}}))
+        return MOE_ERR_INVALID_ARG;
     const QuantArgs a = {x, inv, static_cast<uint8_t*>(q), scales, nullptr, M, K, H, P, fp8 == MOE_DT_E5M2};
     return launched(launch_quantize_rows(a, QS_ROWS, dtype == MOE_DT_FP32, sm_count(), (cudaStream_t)stream));
 }
@@ -191,7 +224,8 @@ moe_status_t moe_quantize_blocks(const void* w, int dtype, int E, int N, int C, 
     if (E == 0) return MOE_OK;
     if (bad_ptr(w) || bad_ptr(q) || bad_ptr(scales)) return MOE_ERR_INVALID_ARG;
     const size_t n = (size_t)E * N * C;
-    if (overlaps(w, n * dt_bytes(dtype), q, n)) return MOE_ERR_INVALID_ARG;
+    if (clash({{q, n}, {scales, scale_bytes((size_t)E * cdiv(N, kQBlock), C)}}, {{w, n * dt_bytes(dtype)}}))
+        return MOE_ERR_INVALID_ARG;
     return launched(launch_quantize_blocks(w, dtype == MOE_DT_FP32, E, N, C, fp8 == MOE_DT_E5M2,
                                            static_cast<uint8_t*>(q), scales, (cudaStream_t)stream));
 }
@@ -207,7 +241,9 @@ moe_status_t moe_quantize_columns(const void* x, int dtype, int P, int C, const 
     if (P == 0) return MOE_OK;
     if (bad_ptr(x) || bad_ptr(q) || bad_ptr(scales)) return MOE_ERR_INVALID_ARG;
     const int blocks = moe_column_blocks(P, E);
-    if (overlaps(x, (size_t)P * C * dt_bytes(dtype), q, (size_t)blocks * kQBlock * C)) return MOE_ERR_INVALID_ARG;
+    if (clash({{q, (size_t)blocks * kQBlock * C}, {scales, (size_t)blocks * C * sizeof(float)}},
+              {{x, (size_t)P * C * dt_bytes(dtype)}, {offsets, offset_bytes(E)}}))
+        return MOE_ERR_INVALID_ARG;
     return launched(launch_quantize_columns(x, dtype == MOE_DT_FP32, P, C, offsets, E, fp8 == MOE_DT_E5M2,
                                             static_cast<uint8_t*>(q), scales, blocks, sm_count(),
                                             (cudaStream_t)stream));
@@ -225,7 +261,7 @@ moe_status_t moe_activation(const void* y, int dtype, int act, int P, int I, voi
     if (bad_ptr(y) || bad_ptr(h)) return MOE_ERR_INVALID_ARG;
     const bool swiglu = act == MOE_ACT_SWIGLU;
     const size_t n = (size_t)P * I * dt_bytes(dtype);
-    if (overlaps(y, swiglu ? 2 * n : n, h, n)) return MOE_ERR_INVALID_ARG;
+    if (clash({{h, n}}, {{y, swiglu ? 2 * n : n}})) return MOE_ERR_INVALID_ARG;
     const QuantArgs a = {y, nullptr, nullptr, nullptr, h, P, 1, I, P, 0};
     return launched(launch_quantize_rows(a, swiglu ? QS_SWIGLU : QS_RELU2, dtype == MOE_DT_FP32, sm_count(),
                                          (cudaStream_t)stream));
@@ -239,7 +275,9 @@ moe_status_t moe_activation_quantize(const void* y, int dtype, int act, int P, i
     if (P == 0) return MOE_OK;
     if (bad_ptr(y) || bad_ptr(q) || bad_ptr(scales)) return MOE_ERR_INVALID_ARG;
     const bool swiglu = act == MOE_ACT_SWIGLU;
-    if (overlaps(y, (size_t)P * I * dt_bytes(dtype) * (swiglu ? 2 : 1), q, (size_t)P * I)) return MOE_ERR_INVALID_ARG;
+    const size_t n = (size_t)P * I;
+    if (clash({{q, n}, {scales, scale_bytes(P, I)}}, {{y, n * dt_bytes(dtype) * (swiglu ? 2 : 1)}}))
+        return MOE_ERR_INVALID_ARG;
     const QuantArgs a = {y, nullptr, static_cast<uint8_t*>(q), scales, nullptr, P, 1, I, P, fp8 == MOE_DT_E5M2};
     return launched(launch_quantize_rows(a, swiglu ? QS_SWIGLU : QS_RELU2, dtype == MOE_DT_FP32, sm_count(),
                                          (cudaStream_t)stream));
@@ -253,7 +291,7 @@ moe_status_t moe_activation_backward(const void* y, const void* dh, int dtype, i
     if (bad_ptr(y) || bad_ptr(dh) || bad_ptr(dy)) return MOE_ERR_INVALID_ARG;
     const bool swiglu = act == MOE_ACT_SWIGLU;
     const size_t n = (size_t)P * I * dt_bytes(dtype), ny = swiglu ? 2 * n : n;
-    if (overlaps(dy, ny, y, ny) || overlaps(dy, ny, dh, n)) return MOE_ERR_INVALID_ARG;
+    if (clash({{dy, ny}}, {{y, ny}, {dh, n}})) return MOE_ERR_INVALID_ARG;
     return launched(launch_activation_backward(y, dh, dtype == MOE_DT_FP32, swiglu, P, I, dy, sm_count(),
                                                (cudaStream_t)stream));
 }
@@ -312,7 +350,12 @@ moe_status_t moe_product_weight_grad(const void* dyq, const float* dy_scales, in
         return accumulate ? MOE_OK : launched(cudaMemsetAsync(dw, 0, out_bytes, (cudaStream_t)stream));
     if (bad_ptr(dyq) || bad_ptr(dy_scales) || bad_ptr(xq) || bad_ptr(x_scales)) return MOE_ERR_INVALID_ARG;
     const size_t rows = (size_t)B * kQBlock;
-    if (overlaps(dw, out_bytes, dyq, rows * N) || overlaps(dw, out_bytes, xq, rows * C)) return MOE_ERR_INVALID_ARG;
+    if (clash({{dw, out_bytes}}, {{dyq, rows * N},
+                                  {dy_scales, (size_t)B * N * sizeof(float)},
+                                  {xq, rows * C},
+                                  {x_scales, (size_t)B * C * sizeof(float)},
+                                  {offsets, offset_bytes(E)}}))
+        return MOE_ERR_INVALID_ARG;
     ProductArgs a;
     std::memset(&a, 0, sizeof(a));
     a.rows = N;
