@@ -18,14 +18,16 @@ is launched, and a refusal by the library raises ``moe.MoEError``.  Work and new
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional
 
 import torch
 
 from . import moe
-from .moe import ACT, MOE_ERR_DEVICE, MOE_OK, MoEError, _lib
+from .moe import ACT, MOE_ERR_DEVICE, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_OK, MoEError, _lib
 
 BLOCK = 128  # MOE_QUANT_BLOCK
+MAX_ROWS = 65536 * 8  # MOE_MAX_ROWS
 DTYPES = {torch.bfloat16: moe.DT_BF16, torch.float32: moe.DT_FP32}
 FP8 = {torch.float8_e4m3fn: moe.DT_E4M3, torch.float8_e5m2: moe.DT_E5M2}
 
@@ -68,19 +70,40 @@ def _tensor(name: str, t, device, dtypes, shape):
     return t
 
 
+def _narrow(name: str, t):
+    """``t``'s sizes fit the library's 32-bit arguments."""
+    if t.dim() and max(t.shape) >> 31:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"{name} of shape {tuple(t.shape)}")
+
+
 def _first(name: str, t):
     """The device of an operator's first tensor."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    n = t.numel()
+    if n >> 31 or n == 0:
+        _narrow(name, t)
     return t.device
 
 
+def _count(name: str, n, most: int) -> int:
+    """A number of rows or tokens, at most ``most``."""
+    try:
+        n = operator.index(n)
+    except TypeError:
+        raise ValueError(f"{name}: expected a whole number, got {type(n).__name__}") from None
+    if not 0 <= n <= most:
+        raise MoEError(MOE_ERR_INVALID_ARG if n < 0 else MOE_ERR_UNSUPPORTED, f"{name} {n}")
+    return n
+
+
 def _key(table: dict, key, what: str) -> int:
-    if key not in table:
-        raise ValueError(f"{what}: expected {' or '.join(str(k) for k in table)}, got {key}")
-    return table[key]
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what}: expected {' or '.join(str(k) for k in table)}, got {key}") from None
 
 
 def _blocks(n: int) -> int:
@@ -100,7 +123,10 @@ class _On:
     def __init__(self, device, stream):
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
+                try:
+                    stream = torch.cuda.ExternalStream(operator.index(stream), device=device)
+                except TypeError:
+                    raise ValueError(f"stream: expected a stream or its handle, got {type(stream).__name__}") from None
             if stream.device != device:
                 raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
         self._guards, self._stream, self._device = (), stream, device
@@ -129,7 +155,7 @@ def _out(name, out, shape, dtype, device):
 def _pair(out):
     if out is None:
         return None, None
-    if len(out) != 2:
+    if not isinstance(out, (tuple, list)) or len(out) != 2:
         raise ValueError("out: expected two tensors")
     return out
 
@@ -142,13 +168,26 @@ def _call(name: str, *args):
 
 def _slots(inv, M: int, device):
     _tensor("inv", inv, device, (torch.int32,), (None,))
+    n = inv.numel()
+    if n >> 31:
+        _narrow("inv", inv)
     if M == 0:
-        if inv.numel():
+        if n:
             raise ValueError("inv: expected no slots for no tokens")
         return 1
-    if inv.numel() == 0 or inv.numel() % M:
-        raise ValueError(f"inv: expected a multiple of {M} slots, got {inv.numel()}")
-    return inv.numel() // M
+    if n == 0 or n % M:
+        raise ValueError(f"inv: expected a multiple of {M} slots, got {n}")
+    return n // M
+
+
+def _experts(offsets) -> int:
+    """The number of experts that offsets (None: one expert) belong to."""
+    if offsets is None:
+        return 1
+    if not isinstance(offsets, torch.Tensor):
+        raise ValueError(f"offsets: expected a tensor, got {type(offsets).__name__}")
+    _narrow("offsets", offsets)
+    return max(1, offsets.numel() - 1)
 
 
 def _offsets(offsets, E: int, device):
@@ -167,7 +206,7 @@ def dispatch(x: torch.Tensor, inv: torch.Tensor, rows: Optional[int] = None, out
     _tensor("x", x, dev, DTYPES, (None, None))
     M, H = x.shape
     K = _slots(inv, M, dev)
-    P = inv.numel() if rows is None else rows
+    P = inv.numel() if rows is None else _count("rows", rows, MAX_ROWS)
     with _On(dev, stream) as s:
         out = _out("out", out, (P, H), x.dtype, dev)
         _call("moe_dispatch", x.data_ptr(), DTYPES[x.dtype], M, K, H, inv.data_ptr(), P, out.data_ptr(), s)
@@ -176,7 +215,7 @@ def dispatch(x: torch.Tensor, inv: torch.Tensor, rows: Optional[int] = None, out
 
 def dispatch_backward(dxs: torch.Tensor, inv: torch.Tensor, M: int, out=None, stream=None):
     """Gradient of ``dispatch``: rows [P, H] summed per token into [M, H]."""
-    return _combine(dxs, inv, None, M, out, stream)
+    return _combine(dxs, inv, None, _count("M", M, MAX_ROWS), out, stream)
 
 
 def dispatch_quantize(x: torch.Tensor, inv: torch.Tensor, rows: Optional[int] = None,
@@ -188,7 +227,7 @@ def dispatch_quantize(x: torch.Tensor, inv: torch.Tensor, rows: Optional[int] = 
     fp8 = _key(FP8, dtype, "dtype")
     M, H = x.shape
     K = _slots(inv, M, dev)
-    P = inv.numel() if rows is None else rows
+    P = inv.numel() if rows is None else _count("rows", rows, MAX_ROWS)
     q, sc = _pair(out)
     with _On(dev, stream) as s:
         q = _out("out[0]", q, (P, H), dtype, dev)
@@ -215,6 +254,8 @@ def _combine(ys, inv, weights, M, out, stream):
 def combine(ys: torch.Tensor, inv: torch.Tensor, weights: torch.Tensor, out=None, stream=None):
     """The experts' rows [P, H] weighted by [M, K] and summed per token into [M, H] (moe_combine)."""
     _first("weights", weights)
+    if weights.dim() != 2:
+        raise ValueError(f"weights: expected two dimensions, got {weights.dim()}")
     return _combine(ys, inv, weights, weights.shape[0], out, stream)
 
 
@@ -226,6 +267,7 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor, inv: torch.Tensor, weig
     _tensor("dy", dy, dev, DTYPES, (None, None))
     M, H = dy.shape
     _tensor("ys", ys, dev, (dy.dtype,), (None, H))
+    _narrow("ys", ys)
     K = _slots(inv, M, dev)
     _tensor("weights", weights, dev, (torch.float32,), (M, K if M else None))
     dys, dw = _pair(out)
@@ -283,7 +325,7 @@ def quantize_columns(x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
     _tensor("x", x, dev, DTYPES, (None, None))
     fp8 = _key(FP8, dtype, "dtype")
     P, C = x.shape
-    E = 1 if offsets is None else max(1, offsets.numel() - 1)
+    E = _experts(offsets)
     off = _offsets(offsets, E, dev)
     B = column_blocks(P, E)
     q, sc = _pair(out)
@@ -351,6 +393,8 @@ def _operands(names, q, sc, wq, ws, offsets, columns: int):
     dev = _first(names[0], q)
     _tensor("wq", wq, dev, (torch.float8_e4m3fn,), (None, None, None))
     E, N, C = wq.shape
+    if (E | N | C) >> 31:
+        _narrow("wq", wq)
     _tensor("ws", ws, dev, (torch.float32,), (E, _blocks(N), _blocks(C)))
     _tensor(names[0], q, dev, FP8, (None, wq.shape[columns]))
     _tensor(names[1], sc, dev, (torch.float32,), (q.shape[0], _blocks(q.shape[1])))
@@ -412,9 +456,10 @@ def product_weight_grad(dyq, dys, xq, xs, offsets: Optional[torch.Tensor] = None
         raise ValueError(f"dyq: expected a multiple of {BLOCK} rows, got {dyq.shape[0]}")
     _tensor("dys", dys, dev, (torch.float32,), (B, N))
     _tensor("xq", xq, dev, FP8, (B * BLOCK, None))
+    _narrow("xq", xq)
     C = xq.shape[1]
     _tensor("xs", xs, dev, (torch.float32,), (B, C))
-    E = 1 if offsets is None else max(1, offsets.numel() - 1)
+    E = _experts(offsets)
     off = _offsets(offsets, E, dev)
     dt = _key(DTYPES, out_dtype, "out_dtype")
     if accumulate and out is None:
