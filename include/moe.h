@@ -419,8 +419,9 @@ moe_status_t moe_product_weight_grad(const void* dyq, const float* dy_scales, in
                                      const float* x_scales, int x_fp8, int B, int N, int C, const int32_t* offsets,
                                      int E, int out_dtype, int accumulate, void* dw, void* stream);
 /* Read and clear the products' device error word of the current device (MOE_DEVERR_WAIT_TIMEOUT:
- * a bounded wait gave up and outputs are incomplete).  Synchronises `stream`.  Returns as
- * moe_get_error. */
+ * a bounded wait gave up and outputs are incomplete), in one step: a product on another stream
+ * that sets it meanwhile is reported by this call or by the next.  Synchronises `stream`.  Returns
+ * as moe_get_error. */
 moe_status_t moe_product_get_error(int* code, void* stream);
 
 /* Human-readable name of a status code (static storage). */

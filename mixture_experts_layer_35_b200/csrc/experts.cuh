@@ -262,9 +262,11 @@ cudaError_t launch_product(int kind, int act, const ProductArgs& a, const Produc
 cudaError_t launch_product_few(int kind, int act, int tile_rows, const ProductArgs& a, const ProductMaps& m, int sms,
                                cudaStream_t s);
 cudaError_t launch_weight_grad(const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s);
-// Error words, read and cleared (product_error takes the others' in).
-cudaError_t product_few_error(int* code, cudaStream_t s);
-cudaError_t weight_grad_error(int* code, cudaStream_t s);
+// Addresses of the error words on the current device; and all of them read and cleared, after the
+// work on `s` so far (synchronises it).
+cudaError_t product_error_word(int** p);
+cudaError_t product_few_error_word(int** p);
+cudaError_t weight_grad_error_word(int** p);
 cudaError_t product_error(int* code, cudaStream_t s);
 
 }  // namespace moe

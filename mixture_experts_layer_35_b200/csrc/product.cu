@@ -475,18 +475,8 @@ cudaError_t launch_product(int kind, int act, const ProductArgs& a, const Produc
     return launch_t<PK_FORWARD, 256, 0>(a, m, sms, s);
 }
 
-cudaError_t product_error(int* code, cudaStream_t s) {
-    void* p = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&p, g_product_error);
-    int word = 0;
-    *code = 0;
-    if (e == cudaSuccess) e = take_error(p, &word, s);
-    *code |= word;
-    if (e == cudaSuccess) e = product_few_error(&word, s);
-    *code |= word;
-    if (e == cudaSuccess) e = weight_grad_error(&word, s);
-    *code |= word;
-    return e;
+cudaError_t product_error_word(int** p) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_product_error);
 }
 
 }  // namespace moe

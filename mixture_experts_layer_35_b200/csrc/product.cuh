@@ -152,13 +152,5 @@ cudaError_t prepare_product(Kern kern, size_t smem, bool moves_registers) {
     if (e != cudaSuccess) return e;
     return fa.numRegs < kRegsLaunch ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
-// Reads and clears one translation unit's error word.
-inline cudaError_t take_error(const void* symbol_address, int* code, cudaStream_t s) {
-    void* p = const_cast<void*>(symbol_address);
-    cudaError_t e = cudaMemcpyAsync(code, p, sizeof(int), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, sizeof(int), s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return e;
-}
 
 }  // namespace moe

@@ -592,10 +592,8 @@ cudaError_t launch_product_few(int kind, int act, int rows, const ProductArgs& a
     return launch_rows<PK_FORWARD, 0>(a, m, rows, sms, s);
 }
 
-cudaError_t product_few_error(int* code, cudaStream_t s) {
-    void* p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_few_error);
-    return e == cudaSuccess ? take_error(p, code, s) : e;
+cudaError_t product_few_error_word(int** p) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_few_error);
 }
 
 }  // namespace moe

@@ -357,10 +357,8 @@ cudaError_t launch_weight_grad(const ProductArgs& a, const ProductMaps& m, int s
     return launch_t<128>(a, m, sms, s);
 }
 
-cudaError_t weight_grad_error(int* code, cudaStream_t s) {
-    void* p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_wgrad_error);
-    return e == cudaSuccess ? take_error(p, code, s) : e;
+cudaError_t weight_grad_error_word(int** p) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_wgrad_error);
 }
 
 }  // namespace moe
