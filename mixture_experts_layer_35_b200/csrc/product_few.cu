@@ -79,12 +79,11 @@ struct Cfg {
     static constexpr int kNA = kSwiglu ? 2 : 1;  // weight tiles: gate and up
     static constexpr int kStageBytes = kNA * A_BYTES + NT * BKB;
     static constexpr int kAccCols = kNA * NT;
-    static constexpr int kBufs = kAccCols == 256 ? 2 : 4;
+    static constexpr int kBufs = 4;
     static constexpr int kTmemCols = kBufs * kAccCols;
     // Each half of the epilogue warps takes every other group of 16 rows.
     static constexpr int kGroups = NT / 32;
     static constexpr int kHalf = NT / 2;
-    static constexpr bool kMoveRegs = kAccCols == 256;
     // Ring of scales, one slot per block along the contraction: the rows' times the weight block's.
     // SwiGLU: times the gate's; the up block's; and the next up block's, since 128 up features may
     // start anywhere in a block.
@@ -101,7 +100,8 @@ struct Cfg {
     static constexpr int kFit = (int)((227 * 1024 - 1024 - kMeta - kPartBytes) / kStageBytes);
     static constexpr int kStages = kFit < 16 ? kFit : 16;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kPartBytes + kMeta;
-    static_assert(kAccCols <= 256, "two accumulator buffers must fit");
+    static_assert(NT == 32 || NT == 64, "a scale warp's lane has one row; a lane keeps one row's maximum");
+    static_assert(kTmemCols <= 512, "the accumulator buffers must fit");
     static_assert(kStages >= 3, "ring too shallow");
     static_assert(8 * (2 * kStages + 2 * kBufs + 2 * kSlots + 3) + 8 <= 512, "barrier block");
 };
@@ -198,7 +198,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     auto tile_at = [&](int tile) { return decode<NT>(a, s_off, s_first, nft, tile); };
 
     if (warp < 4) {
-        if (C::kMoveRegs) regs_set_down<kRegsIssue>();
         if (warp == 0) {
             // ------------------------------------------------------------ TMA producer
             if (lane == 0) {
@@ -268,17 +267,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
         } else {
             // ------------------------------------------------------------ scales (warps 2 and 3)
-            // Rows lane + 32 (warp - 2) + 64 i.  Each block's scales are loaded while the block before
-            // is written, up to kSlots blocks ahead of the sums.
-            constexpr int kMine = (NT + 63) / 64;
-            const int r0 = 32 * (warp - 2) + lane;
-            float x[kMine], w[3];
+            // Row r of the tile.  Each block's scales are loaded while the block before is written, up to
+            // kSlots blocks ahead of the sums.
+            const int r = 32 * (warp - 2) + lane;
+            float x = 0.0f, w[3];
             const float *xp = nullptr, *wp = nullptr, *up0 = nullptr, *up1 = nullptr;
             int n = 0, w_step = 1;
             auto load = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    x[i] = r0 + 64 * i < n ? __ldg(xp + (size_t)(64 * i) * a.nbl + kb) : 0.0f;
+                x = r < n ? __ldg(xp + kb) : 0.0f;
                 w[0] = __ldg(wp + (size_t)kb * w_step);
                 if (kSwiglu) {
                     w[1] = __ldg(up0 + kb);
@@ -288,7 +284,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             auto begin_tile = [&](int tile) {
                 const Tile t = tile_at(tile);
                 n = t.n;
-                xp = a.sa + (size_t)(t.row0 + (r0 < n ? r0 : 0)) * a.nbl;
+                xp = a.sa + (size_t)(t.row0 + (r < n ? r : 0)) * a.nbl;
                 const float* we = a.sb + (size_t)t.e * a.wn * a.wk;
                 if (KIND == PK_INPUT_GRAD) {
                     wp = we + t.f0 / BF;
@@ -307,23 +303,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int tile = first_tile(); ok && tile < total; tile = tile_after(tile)) {
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int i = it % C::kSlots;
-                    float now[kMine], wn[3] = {w[0], w[1], w[2]};
-#pragma unroll
-                    for (int k = 0; k < kMine; ++k) now[k] = x[k];
+                    const float now = x, wn[3] = {w[0], w[1], w[2]};
                     if (kb + 1 < kb1) load(kb + 1);
                     else if (tile_after(tile) < total) begin_tile(tile_after(tile));
                     if (!mbar_wait(sempty_bar(i), ((uint32_t)(it / C::kSlots) & 1u) ^ 1u, abort_flag, err)) {
                         ok = false;
                         break;
                     }
-                    float* dst = s_scales + (size_t)i * C::kSlotFloats + r0;
-#pragma unroll
-                    for (int k = 0; k < kMine; ++k) {
-                        if (r0 + 64 * k >= NT) continue;
-                        dst[64 * k] = now[k] * wn[0];
+                    float* dst = s_scales + (size_t)i * C::kSlotFloats + r;
+                    if (r < NT) {
+                        dst[0] = now * wn[0];
                         if (kSwiglu) {
-                            dst[NT + 64 * k] = now[k] * wn[1];
-                            dst[2 * NT + 64 * k] = now[k] * wn[2];
+                            dst[NT] = now * wn[1];
+                            dst[2 * NT] = now * wn[2];
                         }
                     }
                     __syncwarp();
@@ -333,7 +325,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if (C::kMoveRegs) regs_set_up<kRegsEpilogue>();
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(16 * half);
         int it = 0, ntile = 0;
@@ -360,17 +351,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 tc_fence_after();
                 const float* sx = s_scales + (size_t)i * C::kSlotFloats + 16 * half;
                 const uint32_t tb = tq + (uint32_t)(b * C::kAccCols);
-                // Piece p: group p / kNA of the first (gate) or second (up) sums.  Up to four pieces are read
-                // at once; with eight, each is loaded while the one before is added (there are not
-                // the registers for more).
+                // Piece p: group p / kNA of the first (gate) or second (up) sums; all are read at once.
                 constexpr int kPieces = C::kNA * C::kGroups;
-                constexpr bool kAtOnce = kPieces <= 4;
-                constexpr int kVec = kAtOnce ? kPieces : 2;
                 const int pieces = C::kNA * groups;
                 auto column = [&](int p) { return (uint32_t)((p % C::kNA) * NT + 32 * (p / C::kNA)); };
-                uint32_t v[kVec][16];
+                uint32_t v[kPieces][16];
 #pragma unroll
-                for (int p = 0; p < (kAtOnce ? kPieces : 1); ++p)
+                for (int p = 0; p < kPieces; ++p)
                     if (p < pieces) tmem_ld16(tb + column(p), v[p]);
                 if (pieces == 0) {
                     tc_fence_before();
@@ -380,10 +367,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
                     if (p >= pieces) break;
-                    uint32_t(&w)[16] = v[p % kVec];
+                    uint32_t(&w)[16] = v[p];
                     tmem_ld_wait_for(w);
-                    if (!kAtOnce && p + 1 < kPieces && p + 1 < pieces) tmem_ld16(tb + column(p + 1), v[(p + 1) % kVec]);
-                    if (kAtOnce ? p == 0 : p + 1 == pieces) {  // this warp has read the buffer
+                    if (p == 0) {  // this warp has read the buffer
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(tempty_bar(b));
@@ -481,36 +467,28 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         h[i + 1] = relu2_nan(y);
                     }
                 }
-                constexpr int kKeep = (C::kHalf + 31) / 32;
-                uint32_t keep[kKeep];
+                uint32_t keep = 0;  // lane i: of row i
 #pragma unroll
                 for (int i = 0; i < C::kHalf; ++i) {
                     const uint32_t m = __reduce_max_sync(0xffffffffu, f < a.cols ? abs_bits(h[i]) : 0u);
-                    if (i % 32 == 0) keep[i / 32] = m;
-                    else if (i % 32 == lane) keep[i / 32] = m;
+                    if (i == lane) keep = m;
                 }
                 // Two buffers by tile parity: a warp writes one again only after the other warps'
                 // arrivals for the tile between, which follow their reads.
                 uint32_t* am = reinterpret_cast<uint32_t*>(meta + C::kAmax) + (ntile & 1) * 4 * NT + half * C::kHalf;
-#pragma unroll
-                for (int k = 0; k < kKeep; ++k)
-                    if (lane + 32 * k < C::kHalf) am[q * NT + lane + 32 * k] = keep[k];
+                if (lane < C::kHalf) am[q * NT + lane] = keep;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(amax_bar(half));
                 if (!mbar_wait(amax_bar(half), (uint32_t)ntile & 1u, abort_flag, err)) break;
                 float* factors = reinterpret_cast<float*>(meta + C::kFactor) + (warp - 4) * C::kHalf;
-#pragma unroll
-                for (int k = 0; k < kKeep; ++k) {
-                    const int i = lane + 32 * k;
-                    if (i < C::kHalf) {
-                        float scale, factor;
-                        block_scale(max(max(am[i], am[NT + i]), max(am[2 * NT + i], am[3 * NT + i])), fp8_max(a.h_e5m2),
-                                    scale, factor);
-                        factors[i] = factor;
-                        const int row = 32 * (i / 16) + 16 * half + i % 16;
-                        if (q == 0 && row < t.n)
-                            a.out_scales[(size_t)(t.row0 + row) * cdiv(a.cols, kQBlock) + t.f0 / kQBlock] = scale;
-                    }
+                if (lane < C::kHalf) {
+                    float scale, factor;
+                    block_scale(max(max(am[lane], am[NT + lane]), max(am[2 * NT + lane], am[3 * NT + lane])),
+                                fp8_max(a.h_e5m2), scale, factor);
+                    factors[lane] = factor;
+                    const int row = 32 * (lane / 16) + 16 * half + lane % 16;
+                    if (q == 0 && row < t.n)
+                        a.out_scales[(size_t)(t.row0 + row) * cdiv(a.cols, kQBlock) + t.f0 / kQBlock] = scale;
                 }
                 __syncwarp();
                 uint8_t* out = static_cast<uint8_t*>(a.out) + (size_t)t.row0 * a.cols + (f & ~3);
@@ -552,7 +530,7 @@ template <int KIND, int NT, int ACT, bool SPLIT>
 cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s) {
     using C = Cfg<NT, ACT, SPLIT>;
     auto kern = few_kernel<KIND, NT, ACT, SPLIT>;
-    const cudaError_t e = prepare_product(kern, C::kSmem, C::kMoveRegs);
+    const cudaError_t e = prepare_product(kern, C::kSmem, false);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)cdiv(a.cols, BF) * (a.P / NT + std::min(a.E, a.P));
     if constexpr (!SPLIT)
