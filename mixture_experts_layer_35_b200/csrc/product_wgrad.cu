@@ -8,13 +8,12 @@
 // lie, 128 rows p a step, so nothing is transposed.  The scales change with every block, so the
 // tensor core sums one block at a time into one of several TMEM buffers, and the epilogue
 // warps add buffer * sdy * sx to FP32 sums in registers while the next block's MMAs run.
-// With few rows per expert (blocks per expert below 6) the output's bytes bound it: 128-column
-// tiles, whose two boxes per warp drain through the copy engine while the next tile is
-// summed (64 experts x 256 rows x 1024 x 2048, FP32: 162 us with stores by the warps, 119 so).
+// With few rows per expert the output's bytes bound it: its boxes, two per warp, drain through
+// the copy engine while the next tile is summed (64 experts x 256 rows x 1024 x 2048, FP32, 128-column
+// tiles: 162 us with stores by the warps, 119 so).
 // 512 experts x 2560 x 640 are written at 4.6 TB/s; a plain kernel that stores the same boxes of
 // 128 bytes x 32 rows reaches 5.2 to 5.6, whole rows 6.1.  (Rows of 512 bytes as copies of their own:
-// 757 -> 848 us; boxes of eight rows, a row's four close together: 1141.)  With many rows,
-// 256-column tiles.
+// 757 -> 848 us; boxes of eight rows, a row's four close together: 1141.)
 #include "product.cuh"
 
 namespace moe {
@@ -352,9 +351,19 @@ cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaSt
 
 }  // namespace
 
+// By the output and by the blocks that there is room for, rows / 128 + 1 an expert.  Measured, us of
+// a run that lasts, 128- against 256-column tiles, at 128, 384, 640, 1024 and 2048 rows an expert of
+// 64 experts x 1024 x 2048:
+//   FP32           115 / 114, 157 / 164, 215 / 219, 306 / 301, 543 / 523
+//   BF16            94 /  86, 157 / 144, 218 / 200, 307 / 284, 546 / 506
+// (128 experts x 1856 x 2688, 512 x 2560 x 640 and 8 x 4096 x 4096 the same way: FP32 within 4 % below
+// 300 rows, 128 columns up to 8 % faster from 384 to 640, 256 from 1024 on; BF16 256 throughout.)
+// BF16 values that are added to are read and written by the warps: 389 / 395 at 64 rows, 412 / 413
+// at 256, 465 / 461 at 512, 578 / 564 at 1024 (512 x 2560 x 640 with 64 rows: 2387 / 2842).  FP32 added
+// by the copy engine: within 2 % everywhere.
 cudaError_t launch_weight_grad(const ProductArgs& a, const ProductMaps& m, int sms, cudaStream_t s) {
-    if (a.blocks >= 6LL * a.E) return launch_t<256>(a, m, sms, s);
-    return launch_t<128>(a, m, sms, s);
+    if ((a.out_f32 || a.accumulate) && a.blocks < 6LL * a.E) return launch_t<128>(a, m, sms, s);
+    return launch_t<256>(a, m, sms, s);
 }
 
 cudaError_t weight_grad_error_word(int** p) {
