@@ -457,11 +457,16 @@ cudaError_t launch_t(const ProductArgs& a, const ProductMaps& m, int sms, cudaSt
 
 }  // namespace
 
-// By the rows an expert has on average.  Measured on 128 experts of 1280 x 2560, us of a run
-// that lasts, product_few.cu against product.cu: forward 8 rows 80 / 91, 32 rows 89 / 94, 48 rows
-// 96 / 96, 64 rows 127 / 97; input gradient 86 / 94, 95 / 96, 107 / 98, 141 / 100; SwiGLU, whose two
-// tiles of weights share a row tile, 75 / 92, 79 / 94, 84 / 95, 107 / 97.  Tiles of 32 rows while
-// most experts fit one, else of 64.
+// By the rows an expert has on average, which is all that the host knows.  Measured on 128 experts
+// of 1280 x 2560, us of a run that lasts, product_few.cu against product.cu, with equal experts:
+//   rows            8        16        24        32        40        48        56        64
+//   forward     77 / 87   81 / 91   83 / 91   85 / 92   92 / 93   92 / 96   99 / 96  100 / 96
+//   input grad  88 / 93   86 / 93   93 / 94   94 / 91  101 / 98  105 / 98  109 / 99  111 / 96
+//   SwiGLU      74 / 91   75 / 92   76 / 93   77 / 93   82 / 96   83 / 96   89 / 97   92 / 97
+// (SwiGLU's two tiles of weights share a row tile.)  The borders lie below the crossovers because
+// experts are seldom equal, and crowded rows cost product_few.cu more: 16 rows on average, forward,
+// 46 / 52 with all of them on 64 of the experts, 46 / 37 on 32, 45 / 21 on 16, 45 / 18 on 8; 32 rows
+// 52 / 55, 51 / 39, 49 / 33, 49 / 31.  Tiles of 32 rows while most experts fit one, else of 64.
 int product_few_rows(int act, const ProductArgs& a) {
     const long long rows = a.P, e = a.E;
     if (rows >= (act == 1 + MOE_ACT_SWIGLU ? 56 : 36) * e) return 0;
