@@ -355,7 +355,9 @@ moe_status_t moe_combine_backward(const void* dy, const void* ys, int dtype, int
  * FP32 scale s = a / fmax and the values q = round(v * f), f = fmax / a, every operation
  * in FP32 rounded to nearest even (q to the 8-bit type); v is about s * q.  A block with an
  * infinity or a NaN gets a scale that is one, and its values of it become NaN.
- * Feature counts are multiples of 16.  */
+ * The products form the product of two blocks' scales in FP32: it keeps FP32's precision while
+ * the blocks' largest magnitudes multiply to 2^-94 or more, and overflows from 2^145 on (infinity, and
+ * NaN where the block's sum is zero).  Feature counts are multiples of 16.  */
 /* Rows: one scale per row and MOE_QUANT_BLOCK columns (the last block may be shorter).
  *   x [R, C] of `dtype`; q [R, C] of `fp8`; scales [R, ceil(C / 128)] FP32. */
 moe_status_t moe_quantize_rows(const void* x, int dtype, int R, int C, int fp8, void* q, float* scales,

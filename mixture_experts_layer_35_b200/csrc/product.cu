@@ -19,8 +19,8 @@
 // column tiles outer, so that the CTAs at work share weights and rows in L2.  At 16384 x 8192 x
 // 8192 the MMAs alone (no loads, no sums) take 400 ns of a block of 128 x 256 x 128, loads and
 // MMAs 500 (48 KB a block and SM, 14 TB/s out of L2: what bounds it), all of it 570, 2.1 PFLOP/s.
-// 65536 rows of 256 experts x 1024 x 2048: 193 us cold, 232 to 245 in a run that lasts, where the
-// 1000 W cap holds the clock at 1.4 GHz (1.1 PFLOP/s of the rows' own work).
+// 65536 rows of 256 experts x 1024 x 2048, unequal: 193 us cold, 232 to 247 in a run that lasts, where
+// the 1000 W cap holds the clock at 1.4 GHz (1.1 PFLOP/s of the rows' own work); equal: 197.
 #include "product.cuh"
 
 namespace moe {

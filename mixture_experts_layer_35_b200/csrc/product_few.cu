@@ -7,13 +7,13 @@
 // thread holds one feature of every row.  Two warps of their own multiply the rows' scales with the
 // weight block's into a ring in shared memory, ahead of the sums, and the epilogue's threads
 // read them as broadcasts.  Those reads compete with the tensor cores' for shared memory: at 256 rows per
-// expert this orientation takes 437 us where product.cu's takes 193 (256 experts x 1024 x 2048).
-// At 8 rows it takes 57 us where product.cu's takes 64 (128 experts; 4.7 TB/s of weights).
+// expert this orientation takes 416 us where product.cu's takes 197 (256 experts x 1024 x 2048).
+// At 8 rows it takes 51 us where product.cu's takes 60 (128 experts; 5.3 TB/s of weights).
 //
 // A call with fewer tiles than half of the SMs (one token, a few experts) splits the contraction
 // over a cluster of two CTAs: each sums its half of the blocks, the second writes its FP32 sums into
-// the first one's shared memory, and that one adds them.  One token of top-8, H 2048, I 512:
-// forward 10.8 -> 9.9 us, SwiGLU 14.0 -> 11.8 (clusters of four: 9.9 and 11.5).
+// the first one's shared memory, and that one adds them.  One token of top-8, H 2048, I 512,
+// captured: forward 10.9 -> 9.9 us, SwiGLU 13.7 -> 11.7.
 #include "product.cuh"
 
 namespace moe {

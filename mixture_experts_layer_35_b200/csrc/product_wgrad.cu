@@ -10,7 +10,7 @@
 // warps add buffer * sdy * sx to FP32 sums in registers while the next block's MMAs run.
 // With few rows per expert the output's bytes bound it: its boxes, two per warp, drain through
 // the copy engine while the next tile is summed (64 experts x 256 rows x 1024 x 2048, FP32, 128-column
-// tiles: 162 us with stores by the warps, 119 so).
+// tiles: 162 us with stores by the warps, 119 to 125 so).
 // 512 experts x 2560 x 640 are written at 4.6 TB/s; a plain kernel that stores the same boxes of
 // 128 bytes x 32 rows reaches 5.2 to 5.6, whole rows 6.1.  (Rows of 512 bytes as copies of their own:
 // 757 -> 848 us; boxes of eight rows, a row's four close together: 1141.)

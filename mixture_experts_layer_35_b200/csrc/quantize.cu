@@ -7,7 +7,10 @@
 //   columns   128 x 1 inside each expert: the operands of the weight gradient (contraction over rows)
 //   blocks    128 x 128: weights
 // Every value is read once, kept in registers between the maximum and the rounding, and
-// written once; all of them are bound by memory.
+// written once; all of them are bound by memory.  Measured: rows 32768 x 2048 44 us (71 % of the copy
+// rate), quantised dispatch of 8192 x 2560, top 10, 52 us (77 %), columns 24570 x 1856 of 128 experts 36.6 us
+// (58 %), blocks 128 x 1856 x 2688 322 us (92 %); SwiGLU of 32768 x 512 18 us (85 %), to 8 bits 19 us (70 %), its
+// gradient 30 us (88 %); ReLU^2 of 24576 x 1856 31 us (92 %).
 #include "experts.cuh"
 
 namespace moe {

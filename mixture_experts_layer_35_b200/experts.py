@@ -13,7 +13,12 @@ Argument marshalling only, as in ``moe``: every operator is one CUDA kernel of l
 Tensors must be contiguous, 16-byte aligned and all on one CUDA device, which need not be
 the current one; a wrong type, shape, device or layout raises ValueError before anything
 is launched, and a refusal by the library raises ``moe.MoEError``.  Work and new outputs belong to
-``stream`` (default: the device's current stream).
+``stream`` (default: the device's current stream); inputs must be ready there, and must not be freed for
+another stream before that work is done.
+
+Nothing is recorded for autograd: an input that requires grad is read as data, no output requires grad, and a
+write to ``out`` is not counted as a change.  Gradients are calls of their own (``*_backward``, ``*_grad``), to
+be made by the training step or from a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
