@@ -131,3 +131,11 @@ def test_training_step_with_a_row_limit():
     slot = perm.long()
     assert torch.equal(drows, (rw[slot[:R] % M, slot[:R] // M][:, None] * dy[slot[:R] % M].float()).to(BF))
     assert (drw == 0).all()
+
+
+@pytest.mark.parametrize("P", [1, 128, 256, 300])
+def test_blocks_without_rows_and_without_offsets_are_zeros(P):
+    B = ex.column_blocks(P, 1)
+    q, s = ex.quantize_columns(T.randn((P, 48), T.gen(P), BF), out=_nan_room(B, 48, T.E4))
+    n = -(-P // 128)
+    assert (s[:n] > 0).all() and (s[n:] == 0).all() and (q[P:].view(torch.uint8) == 0).all()
